@@ -1,0 +1,53 @@
+// The 4-bit cache's row layout and the bounds shared by its kernels (see spatten.h).
+#pragma once
+
+#include "common.cuh"
+
+namespace spt {
+
+constexpr int kKv4Group = 32;   // channels per scale
+
+// bytes of one row's codes, and its scales
+__host__ __device__ constexpr int kv4_row_bytes(int d_h) { return d_h / 2; }
+__host__ __device__ constexpr int kv4_groups(int d_h) { return d_h / kKv4Group; }
+
+int32_t kv4_validate(const spatten_kv4_cache& c);
+
+// Rows of sequence b in a packed block: cu[b] .. cu[b+1]-1 (one row per sequence when cu is NULL).
+// Offsets that decrease or leave [0, total] give an empty sequence; `bad` says so.
+struct PackedRows {
+  int first, n;
+  bool bad;
+};
+__device__ __forceinline__ PackedRows packed_rows(const int32_t* cu, int b, int total) {
+  if (!cu) return {b, 1, false};
+  const int s = cu[b], e = cu[b + 1];
+  if (s < 0 || e < s || e > total) return {0, 0, true};
+  return {s, e - s, false};
+}
+
+// The sequence that owns packed row r: the last b with cu[b] <= r (B sequences; -1: none).
+__device__ __forceinline__ int owner_of_row(const int32_t* cu, int B, int r) {
+  if (!cu) return r < B ? r : -1;
+  int lo = 0, hi = B;   // cu[lo] <= r < cu[hi] is the invariant sought
+  if (r < cu[0] || r >= cu[B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A row count from the device, held to [0, most]; a count outside is reported.
+__device__ __forceinline__ int clamp_len(int n, int most, int32_t* status) {
+  if (n < 0 || n > most) {
+    report(status, SPATTEN_E_INDEX);
+    n = n < 0 ? 0 : most;
+  }
+  return n;
+}
+
+__device__ __forceinline__ float bf16_bits_to_float(uint32_t b) { return __uint_as_float(b << 16); }
+
+}  // namespace spt

@@ -1,0 +1,96 @@
+"""Device state of a generation over the 4-bit cache: its planes, row counts, workspaces and the calls
+that use them (``spatten_prompt_attention``, ``spatten_kv4_append`` / ``_attention`` / ``_evict`` /
+``_read``).  Argument marshalling only -- every step runs in the library's kernels.
+
+    st = KV4State(B, H, H_kv, d_h, cap)
+    o = st.prompt(q, k, v, cu)             # causal attention of packed prompts; fills the cache
+    st.evict(keep, recent)                 # keep the rows with the most accumulated weight
+    o = st.step(q, k, v)                   # one token per sequence: append, attend
+    o = st.resume(q, k, v, cu, cu_kv, rows)   # prompts that go on over the cached rows
+
+Calls run on torch's current stream.  The counts live on the device, so ``step`` and ``evict`` can be
+captured in a CUDA graph and replayed.
+"""
+import torch
+
+from . import spatten as S
+
+
+class KV4State:
+    """A cache of ``cap`` rows per (sequence, key/value head) for ``B`` sequences of ``H`` query heads.
+
+    Tensors a caller may look at: ``k_codes``, ``k_scale``, ``v_codes``, ``v_scale`` (the planes),
+    ``weight`` (accumulated attention weight), ``pos`` (token positions), ``len`` (rows held), ``seen``
+    (next position), ``status`` (first device-side error, 0 = none)."""
+
+    def __init__(self, B, H, H_kv, d_h, cap, device="cuda"):
+        self.B, self.H, self.H_kv, self.d_h, self.cap = B, H, H_kv, d_h, cap
+        z = lambda *shape, dt: torch.zeros(shape, dtype=dt, device=device)
+        self.k_codes, self.v_codes = (z(B, H_kv, cap, d_h // 2, dt=torch.uint8) for _ in range(2))
+        self.k_scale, self.v_scale = (z(B, H_kv, cap, d_h // 32, dt=torch.bfloat16) for _ in range(2))
+        self.weight, self.pos = z(B, H_kv, cap, dt=torch.float32), z(B, H_kv, cap, dt=torch.int32)
+        self.len, self.seen = z(B, dt=torch.int32), z(B, dt=torch.int32)
+        self.status = z(1, dt=torch.int32)
+        self.cache = S.make_kv4_cache(self.k_codes, self.k_scale, self.v_codes, self.v_scale, self.weight, self.pos)
+        self._ws = {}
+
+    def _workspace(self, key, nbytes):
+        """A workspace of the state's own for one kind of call: calls of one state run in order.  One that
+        becomes too small stays alive, since a captured graph may hold its address."""
+        held = self._ws.setdefault(key, [])
+        if not held or held[-1].numel() < nbytes:
+            held.append(torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.k_codes.device))
+        return held[-1]
+
+    def append(self, k, v, cu=None):
+        """Quantize rows k, v [rows, H_kv, d_h] behind each sequence's rows (cu None: one row each)."""
+        if k.shape != v.shape or k.stride() != v.stride() or tuple(k.shape[1:]) != (self.H_kv, self.d_h) or (
+                k.stride(2) != 1 or (self.H_kv > 1 and k.stride(1) != self.d_h)):
+            raise ValueError("k and v are [rows, H_kv, d_h] alike, with the heads of a row contiguous")
+        if k.dtype != v.dtype:
+            raise TypeError("k and v have one dtype")
+        S.kv4_append(self.cache, k, v, S._row_stride(k), k.shape[0], self.len, self.len, self.seen, self.seen, cu=cu,
+                     dev_status=self.status)
+
+    def prompt(self, q, k, v, cu, o=None):
+        """Causal attention of packed prompts (rows cu[b] .. cu[b+1]-1 are sequence b's) into an empty
+        cache: returns the outputs, appends the rows and adds their attention weights."""
+        self.append(k, v, cu)
+        return self._attention(q, k, v, cu, None, o)
+
+    def resume(self, q, k, v, cu, cu_kv, rows, o=None):
+        """Packed prompts that go on over the cached rows.  cu_kv [B + 1] are the offsets of each
+        sequence's cached and new rows together, ``rows`` their number in all.  Every row, the new ones
+        too, takes part as the value its codes stand for."""
+        self.append(k, v, cu)
+        kk, vv = (torch.zeros((rows, self.H_kv, self.d_h), dtype=q.dtype, device=q.device) for _ in range(2))
+        S.kv4_read(self.cache, cu_kv, rows, kk, vv, self.H_kv * self.d_h, dev_status=self.status)
+        return self._attention(q, kk, vv, cu, cu_kv, o)
+
+    def _attention(self, q, k, v, cu, cu_kv, o):
+        o = torch.empty_like(q) if o is None else o
+        a = S.make_prompt_args(q, k, v, o, cu, cu_kv, weight=self.weight, dev_status=self.status)
+        nb = S.prompt_workspace_size(a)
+        S.prompt_attention(a, self._workspace("prompt", nb), nb)
+        return o
+
+    def attend(self, q, o=None, n_max=None, update_weight=True):
+        """Attention of one query row per sequence, q [B, H, d_h], over the cached rows."""
+        o = torch.empty_like(q) if o is None else o
+        a = S.make_kv4_attn_args(self.cache, q, o, self.len, self.cap if n_max is None else n_max, update_weight,
+                                 dev_status=self.status)
+        nb = S.kv4_attention_workspace_size(a)
+        S.kv4_attention(a, self._workspace("attend", nb), nb)
+        return o
+
+    def step(self, q, k, v, o=None, n_max=None):
+        """One token per sequence: append its key and value rows [B, H_kv, d_h], then attend."""
+        self.append(k, v)
+        return self.attend(q, o, n_max)
+
+    def evict(self, keep, recent=0, n_max=None):
+        """Keep each head's ``keep`` rows with the most accumulated weight (and the last ``recent``)."""
+        n_max = self.cap if n_max is None else n_max
+        nb = S.kv4_evict_workspace_size(self.cache, n_max, keep)
+        S.kv4_evict(self.cache, self.cache, self.len, self.len, self.seen, n_max, keep, recent,
+                    self._workspace("evict", nb), nb, self.status)

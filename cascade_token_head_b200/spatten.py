@@ -65,6 +65,24 @@ class cascade_io(C.Structure):
                 ("trace_head_imp", vp), ("trace_flags", vp), ("attn_events", C.POINTER(vp))]
 
 
+class prompt_args(C.Structure):
+    _fields_ = [("B", i32), ("H", i32), ("H_kv", i32), ("d_h", i32), ("total_q", i32), ("total_kv", i32),
+                ("cu_q", vp), ("cu_kv", vp), ("dtype", i32), ("q", vp), ("q_ld_tok", i64),
+                ("k", vp), ("v", vp), ("kv_ld_tok", i64), ("o", vp), ("o_ld_tok", i64), ("sm_scale", f32),
+                ("weight", vp), ("weight_ld_seq", i64), ("weight_ld_head", i64), ("weight_cap", i32),
+                ("dev_status", vp), ("kernel", i32)]
+
+
+class kv4_cache(C.Structure):
+    _fields_ = [("B", i32), ("H_kv", i32), ("d_h", i32), ("cap", i32),
+                ("k_codes", vp), ("k_scale", vp), ("v_codes", vp), ("v_scale", vp), ("weight", vp), ("pos", vp)]
+
+
+class kv4_attn_args(C.Structure):
+    _fields_ = [("cache", kv4_cache), ("H", i32), ("q", vp), ("dtype", i32), ("q_ld", i64), ("o", vp), ("o_ld", i64),
+                ("len", vp), ("n_max", i32), ("sm_scale", f32), ("update_weight", i32), ("dev_status", vp)]
+
+
 lib.spatten_abi_version.restype = i32
 lib.spatten_status_string.restype = C.c_char_p
 lib.spatten_status_string.argtypes = [i32]
@@ -92,6 +110,22 @@ lib.spatten_cascade_workspace_size.restype = sz
 lib.spatten_cascade_workspace_size.argtypes = [C.POINTER(cascade_cfg)]
 lib.spatten_cascade_forward.restype = i32
 lib.spatten_cascade_forward.argtypes = [C.POINTER(cascade_cfg), C.POINTER(layer_weights), C.POINTER(cascade_io), vp, sz, vp]
+lib.spatten_prompt_workspace_size.restype = sz
+lib.spatten_prompt_workspace_size.argtypes = [C.POINTER(prompt_args)]
+lib.spatten_prompt_attention.restype = i32
+lib.spatten_prompt_attention.argtypes = [C.POINTER(prompt_args), vp, sz, vp]
+lib.spatten_kv4_append.restype = i32
+lib.spatten_kv4_append.argtypes = [C.POINTER(kv4_cache), vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp]
+lib.spatten_kv4_read.restype = i32
+lib.spatten_kv4_read.argtypes = [C.POINTER(kv4_cache), vp, vp, i32, vp, vp, i32, i64, vp, vp]
+lib.spatten_kv4_attention_workspace_size.restype = sz
+lib.spatten_kv4_attention_workspace_size.argtypes = [C.POINTER(kv4_attn_args)]
+lib.spatten_kv4_attention.restype = i32
+lib.spatten_kv4_attention.argtypes = [C.POINTER(kv4_attn_args), vp, sz, vp]
+lib.spatten_kv4_evict_workspace_size.restype = sz
+lib.spatten_kv4_evict_workspace_size.argtypes = [C.POINTER(kv4_cache), i32, i32]
+lib.spatten_kv4_evict.restype = i32
+lib.spatten_kv4_evict.argtypes = [C.POINTER(kv4_cache), C.POINTER(kv4_cache), vp, vp, vp, i32, i32, i32, vp, sz, vp, vp]
 
 # every extern "C" symbol of include/spatten.h
 EXPORTS = ["spatten_abi_version", "spatten_status_string", "spatten_last_cuda_error",
@@ -99,7 +133,10 @@ EXPORTS = ["spatten_abi_version", "spatten_status_string", "spatten_last_cuda_er
            "spatten_attention_workspace_size", "spatten_attention_layer", "spatten_attention_layer_noalloc",
            "spatten_topk_workspace_size",
            "spatten_topk_select", "spatten_gather_kept", "spatten_cascade_workspace_size",
-           "spatten_cascade_forward", "spatten_selftest_exp2_poly", "spatten_set_wait_limit"]
+           "spatten_cascade_forward", "spatten_selftest_exp2_poly", "spatten_set_wait_limit",
+           "spatten_prompt_workspace_size", "spatten_prompt_attention", "spatten_kv4_append", "spatten_kv4_read",
+           "spatten_kv4_attention_workspace_size", "spatten_kv4_attention", "spatten_kv4_evict_workspace_size",
+           "spatten_kv4_evict"]
 
 
 class SpattenError(RuntimeError):
@@ -216,3 +253,122 @@ def make_cfg(mode, B, T, D, H, d_h, L, dtype, token_keep, head_keep, quant, thet
         c.head_keep[l] = head_keep[l] if head_keep is not None else H
     c.quant, c.refetch_threshold, c.sm_scale = int(quant), float(theta), float(sm_scale)
     return c
+
+
+# ---- prompts and the 4-bit cache --------------------------------------------------------------------
+def make_prompt_args(q, k, v, o, cu_q, cu_kv=None, weight=None, sm_scale=0.0, dev_status=None,
+                     kernel=ATTN_AUTO) -> prompt_args:
+    """Arguments of ``prompt_attention`` from torch tensors: q, o [rows, H, d_h] and k, v [rows, H_kv, d_h]
+    (the heads of a row contiguous, the rows at any stride), cu_q, cu_kv int32 [B + 1], weight
+    float32 [B, H_kv, n].  The tensors are kept alive by the result."""
+    for t in (q, k, v, o):
+        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("q, k, v and o are [rows, heads, d_h] with the heads of a row contiguous")
+    if q.shape != o.shape or k.shape != v.shape or k.shape[2] != q.shape[2] or k.stride(0) != v.stride(0):
+        raise ValueError("q and o, and k and v, have the same shapes, and k and v the same row stride")
+    if not (q.dtype == k.dtype == v.dtype == o.dtype):
+        raise TypeError("q, k, v and o have one dtype")
+    a = prompt_args()
+    a.B, a.H, a.H_kv, a.d_h = _i32_vector(cu_q, "cu_q") - 1, q.shape[1], k.shape[1], q.shape[2]
+    if cu_kv is not None and _i32_vector(cu_kv, "cu_kv") != a.B + 1:
+        raise ValueError("cu_kv and cu_q have the same length")
+    a.total_q, a.total_kv, a.cu_q, a.cu_kv, a.dtype = q.shape[0], k.shape[0], ptr(cu_q), ptr(cu_kv), dtype_code(q)
+    a.q, a.q_ld_tok, a.k, a.v, a.kv_ld_tok = ptr(q), _row_stride(q), ptr(k), ptr(v), _row_stride(k)
+    a.o, a.o_ld_tok, a.sm_scale, a.dev_status, a.kernel = ptr(o), _row_stride(o), sm_scale, ptr(dev_status), kernel
+    if weight is not None:
+        _dense_f32(weight, (a.B, a.H_kv), "weight")
+        a.weight, a.weight_ld_seq, a.weight_ld_head, a.weight_cap = (
+            ptr(weight), weight.stride(0), weight.stride(1), weight.shape[2])
+    a._keep = (q, k, v, o, cu_q, cu_kv, weight, dev_status)
+    return a
+
+
+def _row_stride(t) -> int:
+    """Elements between rows; a block of at most one row has none of its own."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _i32_vector(t, name) -> int:
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} is a contiguous int32 vector")
+    return t.shape[0]
+
+
+def _dense_f32(t, lead, name):
+    import torch
+    if t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != tuple(lead) or t.stride(2) != 1:
+        raise TypeError(f"{name} is float32 [{lead[0]}, {lead[1]}, n] with contiguous rows")
+
+
+def prompt_workspace_size(args: prompt_args) -> int:
+    return lib.spatten_prompt_workspace_size(C.byref(args))
+
+
+def prompt_attention(args: prompt_args, ws=None, ws_bytes: int = 0, stream=None):
+    check(lib.spatten_prompt_attention(C.byref(args), ptr(ws), ws_bytes, _stream(stream)), "spatten_prompt_attention")
+
+
+def make_kv4_cache(k_codes, k_scale, v_codes, v_scale, weight=None, pos=None) -> kv4_cache:
+    """The description of a 4-bit cache from its tensors: codes uint8 [B, H_kv, cap, d_h / 2], scales
+    bfloat16 [B, H_kv, cap, d_h / 32], weight float32 and pos int32 [B, H_kv, cap] (all contiguous)."""
+    import torch
+    B, H, cap, half = k_codes.shape
+    want = [(k_codes, torch.uint8, (half,)), (v_codes, torch.uint8, (half,)), (k_scale, torch.bfloat16, (half // 16,)),
+            (v_scale, torch.bfloat16, (half // 16,)), (weight, torch.float32, ()), (pos, torch.int32, ())]
+    for t, dt, tail in want:
+        if t is not None and (t.dtype != dt or tuple(t.shape) != (B, H, cap) + tail or not t.is_contiguous()):
+            raise TypeError(f"a cache tensor is not a contiguous {dt} {(B, H, cap) + tail}")
+    c = kv4_cache(B, H, 2 * half, cap, ptr(k_codes), ptr(k_scale), ptr(v_codes), ptr(v_scale), ptr(weight), ptr(pos))
+    c._keep = (k_codes, k_scale, v_codes, v_scale, weight, pos)
+    return c
+
+
+def kv4_append(cache: kv4_cache, k, v, ld_tok, total, len, len_out, seen=None, seen_out=None, cu=None, dtype=None,
+               dev_status=None, stream=None):
+    dt = dtype_code(k) if dtype is None else dtype
+    check(lib.spatten_kv4_append(C.byref(cache), ptr(k), ptr(v), dt, ld_tok, total, ptr(cu), ptr(len), ptr(len_out),
+                                 ptr(seen), ptr(seen_out), ptr(dev_status), _stream(stream)), "spatten_kv4_append")
+
+
+def kv4_read(cache: kv4_cache, cu, total, k_out, v_out, ld_tok, row0=None, dtype=None, dev_status=None, stream=None):
+    dt = dtype_code(k_out if k_out is not None else v_out) if dtype is None else dtype
+    check(lib.spatten_kv4_read(C.byref(cache), ptr(cu), ptr(row0), total, ptr(k_out), ptr(v_out), dt, ld_tok,
+                               ptr(dev_status), _stream(stream)), "spatten_kv4_read")
+
+
+def make_kv4_attn_args(cache: kv4_cache, q, o, len, n_max, update_weight=True, sm_scale=0.0,
+                       dev_status=None) -> kv4_attn_args:
+    """Arguments of ``kv4_attention``: q, o [B, H, d_h] (the heads of a row contiguous), len int32 [B]."""
+    for t in (q, o):
+        if t.dim() != 3 or tuple(t.shape) != (cache.B, q.shape[1], cache.d_h) or t.stride(2) != 1 or (
+                t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("q and o are [B, H, d_h] with the heads of a row contiguous")
+    if q.dtype != o.dtype:
+        raise TypeError("q and o have one dtype")
+    if _i32_vector(len, "len") != cache.B:
+        raise ValueError("len has one entry per sequence")
+    a = kv4_attn_args()
+    a.cache, a.H, a.q, a.dtype, a.q_ld = cache, q.shape[1], ptr(q), dtype_code(q), _row_stride(q)
+    a.o, a.o_ld, a.len, a.n_max, a.sm_scale = ptr(o), _row_stride(o), ptr(len), n_max, sm_scale
+    a.update_weight, a.dev_status = int(update_weight), ptr(dev_status)
+    a._keep = (cache, q, o, len, dev_status)
+    return a
+
+
+def kv4_attention_workspace_size(args: kv4_attn_args) -> int:
+    return lib.spatten_kv4_attention_workspace_size(C.byref(args))
+
+
+def kv4_attention(args: kv4_attn_args, ws, ws_bytes: int, stream=None):
+    check(lib.spatten_kv4_attention(C.byref(args), ptr(ws), ws_bytes, _stream(stream)), "spatten_kv4_attention")
+
+
+def kv4_evict_workspace_size(cache: kv4_cache, n_max: int, keep: int) -> int:
+    return lib.spatten_kv4_evict_workspace_size(C.byref(cache), n_max, keep)
+
+
+def kv4_evict(src: kv4_cache, dst: kv4_cache, len, len_out, seen, n_max, keep, recent, ws, ws_bytes: int,
+              dev_status=None, stream=None):
+    check(lib.spatten_kv4_evict(C.byref(src), C.byref(dst), ptr(len), ptr(len_out), ptr(seen), n_max, keep, recent,
+                                ptr(ws), ws_bytes, ptr(dev_status), _stream(stream)), "spatten_kv4_evict")

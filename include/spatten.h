@@ -354,6 +354,159 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
                                 spatten_cascade_io* io, void* ws, size_t ws_bytes, void* stream);
 
 /* =============================================================================================
+ * spatten_prompt_attention -- causal attention over whole prompts: sequences of different lengths
+ * packed into one row block, and grouped heads (H query heads over H_kv key/value heads, query head
+ * h reads key/value head h / (H / H_kv)).  (The paper's generation stage starts from a prompt,
+ * §II "Attention-based NLP models"; the pages give its accumulated probabilities, §II "Cascade
+ * pruning", which `weight` collects here per key/value head for spatten_kv4_evict.)
+ *
+ * Sequence b owns query rows cu_q[b] .. cu_q[b+1]-1 and key rows cu_kv[b] .. cu_kv[b+1]-1 of the
+ * packed blocks.  Its query rows are the last n_q of its n_kv positions (n_kv > n_q: a prompt that
+ * goes on over a history).  Query row i sees the keys j <= i + n_kv - n_q:
+ *   S_ij = sm_scale * q_i . k_j,  P_i = softmax over the visible j,  O_i = sum_j P_ij v_j
+ *   weight[b][h_kv][j] += sum over the group's heads and the rows i of P_ij
+ * A row that sees no key (n_q > n_kv) gets O = 0 and adds nothing.  Sums are made in a fixed order
+ * (reruns are bit-identical).  P enters the product with V as bfloat16 for bfloat16 inputs (as the
+ * values do), float32 for float32 ones; statistics and sums are float32.
+ *  - total_q and total_kv are the rows of the packed blocks; rows outside every sequence are neither
+ *    read nor written.  Offsets that decrease or leave [0, total] are reported (SPATTEN_E_INDEX) and
+ *    their sequence is taken as empty.
+ *  - Infinities and NaN in rows of other sequences, or outside every sequence, change nothing.  Inside
+ *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable.
+ *  - weight rows j >= weight_cap are not written and reported (SPATTEN_E_INDEX).
+ *  - o overlaps none of the inputs.
+ *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
+ *  strides; workspace of spatten_prompt_workspace_size() bytes (0 without weight), which holds only this call's
+ *  intermediates: calls that overlap on the GPU need one each.
+ * ============================================================================================= */
+typedef struct spatten_prompt_args {
+  int32_t B, H, H_kv, d_h;
+  int32_t total_q, total_kv;  /* rows of the packed blocks; 0 rows are allowed                 */
+  const int32_t* cu_q;        /* device [B+1]: first query row of each sequence, then the end  */
+  const int32_t* cu_kv;       /* device [B+1] for the key rows, or NULL: the same as cu_q      */
+  int32_t dtype;              /* q, k, v and o: SPATTEN_F32 or SPATTEN_BF16                     */
+  const void* q;              /* device; q(r,h,d) = q[r*q_ld_tok + h*d_h + d]                   */
+  int64_t q_ld_tok;
+  const void* k;              /* device; k(r,h,d) = k[r*kv_ld_tok + h*d_h + d], v alike         */
+  const void* v;
+  int64_t kv_ld_tok;
+  void* o;                    /* device; o(r,h,d) = o[r*o_ld_tok + h*d_h + d]                   */
+  int64_t o_ld_tok;
+  float sm_scale;             /* <= 0 selects 1/sqrt(d_h)                                      */
+  float* weight;              /* device (+=) or NULL: weight[b*weight_ld_seq + h*weight_ld_head + j] */
+  int64_t weight_ld_seq, weight_ld_head;
+  int32_t weight_cap;         /* rows j < weight_cap exist                                     */
+  int32_t* dev_status;        /* device int32 or NULL                                          */
+  int32_t kernel;             /* spatten_attn_kernel: AUTO, CUDA_CORE or TENSOR_CORE (bfloat16)  */
+} spatten_prompt_args;
+
+size_t spatten_prompt_workspace_size(const spatten_prompt_args* a);
+int32_t spatten_prompt_attention(const spatten_prompt_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* =============================================================================================
+ * The 4-bit cache -- K and V rows of a generation in 4 bits, with rows that can be given up.
+ *
+ * Per (sequence, key/value head) `cap` rows; the first len[b] hold a token each, in any order (a
+ * row's token is pos).  Each row is quantized in groups of 32 channels, on its own:
+ *   s = bfloat16(amax / 7) (1 if that is 0),  code = clamp(rint_half_even(x / s), -7, 7) (IEEE
+ *   float32 divides),  value = s * code.  A non-finite x is stored as 0, left out of the amax and
+ *   reported (SPATTEN_E_NONFINITE).
+ * Layout (device, row-major, the caller's):
+ *   k_codes  uint8 [B][H_kv][cap][d_h/2]   code + 8 in nibbles, low nibble first; the row's 32-bit
+ *            word t*(d_h/32) + g holds channels 32g + 8t .. 32g + 8t + 7
+ *   v_codes  uint8 [B][H_kv][cap][d_h/2]   the row's 16-bit halfword t*(d_h/32) + g holds channels
+ *            32g + 4t .. 32g + 4t + 3
+ *   k_scale, v_scale  bfloat16 [B][H_kv][cap][d_h/32]
+ *   weight   float [B][H_kv][cap]          accumulated attention weight of the row, or NULL
+ *   pos      int32 [B][H_kv][cap]          position of the row's token in its sequence, or NULL
+ * Row counts (len) and the next position of each sequence (seen) are device arrays that the calls
+ * read and write, so that a captured step can be replayed.  Counts outside [0, cap] are clamped and
+ * reported (SPATTEN_E_INDEX).
+ * ============================================================================================= */
+typedef struct spatten_kv4_cache {
+  int32_t B, H_kv, d_h, cap;  /* d_h 64 or 128                                                 */
+  uint8_t* k_codes;
+  uint16_t* k_scale;
+  uint8_t* v_codes;
+  uint16_t* v_scale;
+  float* weight;
+  int32_t* pos;
+} spatten_kv4_cache;
+
+/* ---------------------------------------------------------------------------------------------
+ * spatten_kv4_append -- quantize new rows of K and V behind the rows of every sequence.
+ *  k, v      device, dtype elements; row r of the packed block, head h at [r*ld_tok + h*d_h].
+ *  cu        device int32 [B+1]: sequence b's rows are cu[b] .. cu[b+1]-1 of the block; NULL: one
+ *            row per sequence (total == B).  Rows outside every sequence are ignored.
+ *  len       device int32 [B]: rows already there; new row i goes to row len[b] + i with weight 0
+ *            and pos seen[b] + i.  Rows past cap are dropped and reported (SPATTEN_E_INDEX).
+ *  len_out, seen_out  device int32 [B]: the counts after the call; they may be len and seen
+ *            themselves.  seen and seen_out may both be NULL when the cache has no pos.
+ * --------------------------------------------------------------------------------------------- */
+int32_t spatten_kv4_append(const spatten_kv4_cache* c, const void* k, const void* v, int32_t dtype,
+                           int64_t ld_tok, int32_t total, const int32_t* cu, const int32_t* len,
+                           int32_t* len_out, const int32_t* seen, int32_t* seen_out,
+                           int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * spatten_kv4_read -- rows of the cache as bfloat16 or float32 values (rounded once), packed: rows
+ * cu[b] .. cu[b+1]-1 of k_out and v_out get the cache rows row0[b], row0[b] + 1, ... of sequence b
+ * (row0 NULL: from row 0).  A history read this way is the key block of a prompt that goes on over
+ * it.  Cache rows outside [0, cap) read as 0 and are reported (SPATTEN_E_INDEX); rows of the block
+ * outside every sequence are left as they were.  One of k_out and v_out may be NULL.
+ * --------------------------------------------------------------------------------------------- */
+int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* cu, const int32_t* row0, int32_t total,
+                         void* k_out, void* v_out, int32_t dtype, int64_t ld_tok, int32_t* dev_status,
+                         void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * spatten_kv4_attention -- attention of one new query row per sequence over the cache's rows
+ * j < len[b], with grouped heads as above:
+ *   O = softmax(sm_scale * q . k_j) . v_j;  with update_weight != 0, weight[b][h_kv][j] += the sum of
+ *   the group's probabilities of row j.
+ * O = 0 for an empty sequence.  n_max bounds the lengths of this call (n_max <= cap; a longer
+ * sequence is cut there and reported).  Sums are made in a fixed order (reruns are bit-identical).
+ * Workspace: spatten_kv4_attention_workspace_size() bytes, intermediates of this call only.
+ * --------------------------------------------------------------------------------------------- */
+typedef struct spatten_kv4_attn_args {
+  spatten_kv4_cache cache;
+  int32_t H;                  /* query heads, a multiple of cache.H_kv                          */
+  const void* q;              /* device; q(b,h,d) = q[b*q_ld + h*d_h + d]                        */
+  int32_t dtype;              /* q and o: SPATTEN_F32 or SPATTEN_BF16                           */
+  int64_t q_ld;
+  void* o;                    /* device; o(b,h,d) = o[b*o_ld + h*d_h + d]                        */
+  int64_t o_ld;
+  const int32_t* len;         /* device [B]                                                    */
+  int32_t n_max;
+  float sm_scale;             /* <= 0 selects 1/sqrt(d_h)                                      */
+  int32_t update_weight;
+  int32_t* dev_status;        /* device int32 or NULL                                          */
+} spatten_kv4_attn_args;
+
+size_t spatten_kv4_attention_workspace_size(const spatten_kv4_attn_args* a);
+int32_t spatten_kv4_attention(const spatten_kv4_attn_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * spatten_kv4_evict -- give up the rows with the least accumulated attention weight: of the len[b]
+ * rows of each (sequence, head), the `keep` rows ranked first stay (all of them if there are no
+ * more).  Rows with pos >= seen[b] - recent rank before all others; then by (larger weight, lower
+ * row); a NaN weight ranks last and is reported (SPATTEN_E_NONFINITE).  The kept rows end up in rows
+ * 0 .. keep-1 of dst: a kept row below `keep` keeps its row, and the i-th given-up row below `keep`
+ * is filled from the i-th kept row behind (both ascending), so few rows move.
+ *  src, dst  the same cache (the same pointers and cap: rows move in place), or two whose buffers do
+ *            not overlap (dst.cap >= keep; src is left as it was).  B, H_kv, d_h are equal; src needs
+ *            weight, and pos when recent > 0; dst has weight (pos) if src has.
+ *  len_out   device int32 [B], may be len: min(len, keep).
+ *  seen      device int32 [B], or NULL when recent == 0.
+ *  n_max     bounds the lengths of this call (n_max <= cap; a longer sequence is cut there and reported).
+ * Workspace: spatten_kv4_evict_workspace_size() bytes, intermediates of this call only.
+ * --------------------------------------------------------------------------------------------- */
+size_t spatten_kv4_evict_workspace_size(const spatten_kv4_cache* src, int32_t n_max, int32_t keep);
+int32_t spatten_kv4_evict(const spatten_kv4_cache* src, const spatten_kv4_cache* dst, const int32_t* len,
+                          int32_t* len_out, const int32_t* seen, int32_t n_max, int32_t keep, int32_t recent,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* =============================================================================================
  * Diagnostics
  *
  * spatten_selftest_exp2_poly -- y[i] = 2^x[i] by the polynomial the tensor-core attention kernels
