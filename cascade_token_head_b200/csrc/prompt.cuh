@@ -7,16 +7,24 @@ namespace spt {
 
 struct PromptProblem {
   spatten_prompt_args a;   // sm_scale > 0 and cu_kv set
-  float2* stats;           // [H][total_q]: each row's score maximum (log2 units) and exponential sum, or NULL
+  // with weights only (else NULL).  CUDA cores: [H][total_q] score maximum (log2 units) and exponential
+  // sum of each row.  Tensor cores: the negated maximum and the reciprocal of the sum (0 where a row
+  // sees nothing) in two planes [H][total_q], and the heads' column sums [H][total_kv] (grouped heads).
+  float2* stats;
+  float* stat_m;
+  float* stat_l;
+  float* part;
   uint32_t wait_limit;     // polls of one pipeline wait (tensor-core kernels)
 };
 
 // The sequence and tile of block t, for tiles of `rows` packed rows that start anew at each sequence:
 // tiles are counted from the last sequence's last tile backwards, so that a sequence's late rows, which
-// see the most keys, are started first.  Every warp calls it whole; b = -1 past the last tile.
+// see the most keys, are started first (FRONT: from the first sequence's first tile).  Every warp calls
+// it whole; b = -1 past the last tile.
 struct SeqTile {
   int b, tile;
 };
+template <bool FRONT = false>
 __device__ __forceinline__ SeqTile find_seq_tile(const int32_t* cu, int B, int total, int rows, int t) {
   const int lane = threadIdx.x & 31;
   int all = 0;
@@ -24,8 +32,8 @@ __device__ __forceinline__ SeqTile find_seq_tile(const int32_t* cu, int B, int t
     int c = b0 + lane < B ? (packed_rows(cu, b0 + lane, total).n + rows - 1) / rows : 0;
     all += warp_sum_int(c);
   }
-  int want = all - 1 - t;
-  if (want < 0) return {-1, 0};
+  int want = FRONT ? t : all - 1 - t;
+  if (want < 0 || want >= all) return {-1, 0};
   for (int b0 = 0; b0 < B; b0 += 32) {
     const int c = b0 + lane < B ? (packed_rows(cu, b0 + lane, total).n + rows - 1) / rows : 0;
     int inc = c;
@@ -54,5 +62,7 @@ __device__ __forceinline__ void report_bad_offsets(const spatten_prompt_args& a)
 }
 
 int32_t prompt_simt_launch(const PromptProblem& p, cudaStream_t st);
+int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st);
+bool prompt_tc_supported(const spatten_prompt_args& a);
 
 }  // namespace spt

@@ -1,0 +1,667 @@
+// Prompt attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), bfloat16.
+//
+// Two kernels, and a small third one when several query heads share a key/value head:
+//  OUTPUT  one pass over the visible keys in tiles of 128 with the running maximum and sum of the
+//          softmax.  A CTA owns NQ tiles of 128 query rows that read the same key/value head; each has
+//          a softmax warpgroup (thread r = TMEM lane r = row r), next to one TMA producer warp and one
+//          MMA warp.  S = Q K^T goes to TMEM, P (bfloat16) goes back over the columns of S and is the
+//          TMEM operand of O += P V, so P never touches shared memory.
+//  WEIGHT  weight_j = sum_i exp(S_ij - m_i) / l_i needs final statistics, hence a second pass over the
+//          scores, transposed: S^T = K Q^T puts one key on each TMEM lane, so the sum over the rows stays
+//          inside a thread (no exchange between lanes) and runs in a fixed order.
+//  REDUCE  the heads of a group add up in head order.
+// What bounds them: exponentials (16 per clock and SM; a quarter of the unmasked ones goes to the FMA
+// pipe, exp2_poly.cuh) next to the tensor cores; O's rescaling is skipped while no row's maximum has
+// grown by more than 2^8, which float32 sums and the bfloat16 P bear without loss (P is relative).
+// Every mbarrier wait is bounded: on timeout the CTA reports SPATTEN_E_TIMEOUT, waits for its own
+// copies and MMAs, frees its TMEM and returns.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "attention.cuh"
+#include "exp2_poly.cuh"
+#include "prompt.cuh"
+#include "tc_ptx.cuh"
+
+namespace spt {
+namespace {
+
+using namespace tc;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kKT = 128;          // keys per tile, query rows per tile
+constexpr float kRescale = 8.0f;       // growth of a row's maximum (log2) that makes O be rescaled
+
+// 2^x of a pair; pair Q of every four takes the FMA pipe when Q < 1
+template <int Q>
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+  if constexpr ((Q & 3) < 1) return exp2_poly2(x);
+  else return make_float2(ex2(x.x), ex2(x.y));
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, limit));
+}
+
+// all of a [128 rows x DH] tile: one box per 64 channels
+template <int DH>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < DH / 64; ++c) tma_load_3d(dst + c * kKT * 128, map, c * 64, head, row, bar);
+}
+
+// D[128 x 128] = A B^T over DH channels, both tiles K-major
+template <int DH>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t sA, uint32_t sB) {
+  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+  for (int s = 0; s < DH / 16; ++s) {
+    const uint32_t off = (s >> 2) * (kKT * 128u) + (s & 3) * 32u;
+    mma_f16(d, desc_sw128(sA + off, 16, 1024), desc_sw128(sB + off, 16, 1024), id, s > 0 ? 1u : 0u);
+  }
+}
+// O (+)= P V: P in TMEM (8 columns per 16 keys), V rows MN-major
+template <int DH>
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint32_t sV, uint32_t acc) {
+  constexpr uint32_t id = idesc_bf16(128, DH, false, true);
+#pragma unroll
+  for (int s = 0; s < static_cast<int>(kKT) / 16; ++s)
+    mma_f16_ts(d, p + s * 8, desc_sw128(sV + s * 2048u, kKT * 128u, 1024), id, (acc || s > 0) ? 1u : 0u);
+}
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+// =================================================================================================
+// OUTPUT
+// =================================================================================================
+template <int DH_, int NQ_>
+struct OutCfg {
+  static constexpr int DH = DH_, NQ = NQ_;
+  static constexpr int kStages = 5;                      // K and V tiles in flight, one ring
+  static constexpr uint32_t kTile = kKT * DH * 2u;
+  static constexpr uint32_t oKV = NQ * kTile;
+  static constexpr uint32_t kSmem = oKV + kStages * kTile + 1024u;
+  static constexpr int kThreads = NQ * 128 + 64;
+  static constexpr uint32_t kTmem = NQ * (128 + DH) <= 256 ? 256 : 512;
+  static constexpr int kCtas = kTmem == 256 ? 2 : 1;     // per SM
+  static constexpr uint32_t tS = 0, tO = NQ * 128;
+};
+
+template <int NQ, int NST>
+struct OutBars {
+  uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[NQ], p_ready[NQ], o_full[NQ], v_fix, drain;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
+  constexpr int DH = C::DH, NQ = C::NQ, NST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ OutBars<NQ, NST> bars;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const spatten_prompt_args& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.H / a.H_kv;
+  // NQ = 2: two heads of a group at the same rows, or (odd groups) 256 rows of one head
+  const bool pair_heads = NQ == 2 && (G & 1) == 0;
+  const int tile_rows = NQ == 2 && !pair_heads ? 256 : 128;
+  const int slots = pair_heads ? a.H / 2 : a.H;
+  if (blockIdx.x == 0) report_bad_offsets(a);
+  const SeqTile st = find_seq_tile(a.cu_q, a.B, a.total_q, tile_rows, blockIdx.x / slots);
+  if (st.b < 0) return;
+  const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
+  const PackedRows qr = packed_rows(a.cu_q, st.b, a.total_q), kr = packed_rows(a.cu_kv, st.b, a.total_kv);
+  const int shift = kr.n - qr.n;
+  int head[NQ], row0[NQ], rows[NQ], T[NQ], Tmax = 0;
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) {
+    head[g] = pair_heads ? 2 * slot + g : slot;
+    row0[g] = st.tile * tile_rows + (pair_heads ? 0 : 128 * g);
+    rows[g] = max(0, min(128, qr.n - row0[g]));
+    const int seen = rows[g] ? max(0, min(kr.n, row0[g] + rows[g] + shift)) : 0;   // keys the last row sees
+    T[g] = (seen + static_cast<int>(kKT) - 1) / static_cast<int>(kKT);
+    Tmax = max(Tmax, T[g]);
+  }
+  const int partial = kr.n < Tmax * static_cast<int>(kKT) ? Tmax - 1 : -1;   // the tile that ends past the keys
+
+  constexpr int kProducer = 4 * NQ, kMma = 4 * NQ + 1;
+  if (warp == kMma) tmem_alloc(&tmem_base, C::kTmem);
+  if (tid == 0) {
+    abort_word = 0;
+    mbar_init(&bars.q_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&bars.kv_full[s], 1);
+      mbar_init(&bars.kv_empty[s], 1);
+    }
+    for (int g = 0; g < NQ; ++g) {
+      mbar_init(&bars.s_full[g], 1);
+      mbar_init(&bars.p_ready[g], 128);
+      mbar_init(&bars.o_full[g], 1);
+    }
+    mbar_init(&bars.v_fix, 32);
+    mbar_init(&bars.drain, 1);
+    fence_mbar_init();
+  }
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = tmem_base, wlim = p.wait_limit;
+  bool aborted = false;
+
+  if (warp == kProducer) {
+    int issued = 0;
+    if (lane == 0 && Tmax > 0) {
+      mbar_arrive_expect_tx(&bars.q_full, NQ * C::kTile);
+#pragma unroll
+      for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
+        load_tile<DH>(smem + g * C::kTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
+    }
+    for (int x = 0; x < 2 * Tmax; ++x) {   // K0 V0 K1 V1 ...: the order in which the MMA warp uses them
+      const int s = x % NST, t = x >> 1;
+      const uint32_t ph = (x / NST) & 1;
+      if (!warp_wait(&bars.kv_empty[s], ph ^ 1u, abort_flag, wlim)) {
+        aborted = true;
+        break;
+      }
+      uint8_t* dst = smem + C::oKV + s * C::kTile;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars.kv_full[s], C::kTile);
+        load_tile<DH>(dst, (x & 1) ? &maps.v : &maps.k, hk, kr.first + t * static_cast<int>(kKT), &bars.kv_full[s]);
+      }
+      ++issued;
+      if ((x & 1) && t == partial) {
+        // rows past the sequence's keys meet P = 0: they must be finite, so they become zeros
+        if (!warp_wait(&bars.kv_full[s], ph, abort_flag, wlim)) {
+          aborted = true;
+          break;
+        }
+        const int first = kr.n - t * static_cast<int>(kKT);
+        for (int e = first * 8 + lane; e < static_cast<int>(kKT) * 8; e += 32)
+#pragma unroll
+          for (int c = 0; c < DH / 64; ++c)
+            *reinterpret_cast<uint4*>(dst + c * kKT * 128 + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+        mbar_arrive(&bars.v_fix);
+      }
+    }
+    if (aborted && lane == 0) {   // the copies in flight land before shared memory is given up
+      drain_wait(&bars.q_full, 0);
+      for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.kv_full[x % NST], (x / NST) & 1);
+    }
+  } else if (warp == kMma) {
+    if (lane == 0 && Tmax > 0) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!aborted && !wait_bar(bar, parity, abort_flag, wlim)) aborted = true;
+        return !aborted;
+      };
+      const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::oKV);
+      if (wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0)) {
+        tc_after_sync();
+#pragma unroll
+        for (int g = 0; g < NQ; ++g)
+          if (T[g] > 0) {
+            mma_scores<DH>(tmem + C::tS + g * 128, sQ + g * C::kTile, sKV);
+            mma_commit(&bars.s_full[g]);
+          }
+        mma_commit(&bars.kv_empty[0]);
+      }
+      for (int t = 0; t < Tmax && !aborted; ++t) {
+        const int xv = 2 * t + 1, xk = 2 * t + 2, sv = xv % NST, sk = xk % NST;
+#pragma unroll
+        for (int g = 0; g < NQ; ++g) {
+          if (t >= T[g]) continue;
+          if (!wait(&bars.p_ready[g], t & 1) || !wait(&bars.kv_full[sv], (xv / NST) & 1)) break;
+          if (t == partial && !wait(&bars.v_fix, 0)) break;
+          tc_after_sync();
+          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, sKV + sv * C::kTile, t > 0 ? 1u : 0u);
+          if (t + 1 < T[g]) {
+            if (!wait(&bars.kv_full[sk], (xk / NST) & 1)) break;
+            tc_after_sync();
+            mma_scores<DH>(tmem + C::tS + g * 128, sQ + g * C::kTile, sKV + sk * C::kTile);
+            mma_commit(&bars.s_full[g]);
+          } else {
+            mma_commit(&bars.o_full[g]);
+          }
+        }
+        if (aborted) break;
+        mma_commit(&bars.kv_empty[sv]);
+        if (t + 1 < Tmax) mma_commit(&bars.kv_empty[sk]);
+      }
+      if (aborted) {   // every MMA already issued completes before TMEM is freed
+        mma_commit(&bars.drain);
+        drain_wait(&bars.drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int g = NQ == 1 ? 0 : warp >> 2, r = tid & 127;
+    const int my_row0 = g ? row0[NQ - 1] : row0[0], my_rows = g ? rows[NQ - 1] : rows[0], my_T = g ? T[NQ - 1] : T[0];
+    const int my_head = g ? head[NQ - 1] : head[0];
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's TMEM lanes (32 (warp & 3)) << 16
+    const uint32_t tS = tmem + lanes + C::tS + g * 128, tO = tmem + lanes + C::tO + g * DH;
+    const int last = my_row0 + r + shift;   // the last key this row sees
+    const float c = a.sm_scale * kLog2e;
+    const float2 cc = make_float2(c, c);
+    float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum
+    for (int t = 0; t < my_T; ++t) {
+      if (!warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim)) {
+        aborted = true;
+        break;
+      }
+      tc_after_sync();
+      float v[128];
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, v + ch * 32);
+      tmem_ld_wait();
+      const int j0 = t * static_cast<int>(kKT);
+      const bool masked = j0 + static_cast<int>(kKT) - 1 > my_row0 + shift || j0 + static_cast<int>(kKT) > kr.n;
+      if (masked) {
+        const int lim = min(last, kr.n - 1) - j0;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) v[j] = j <= lim ? v[j] : -INFINITY;
+      }
+      float mx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        mx[k] = v[k];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) mx[k] = fmaxf(mx[k], v[k + 8 * j]);
+      }
+      const float mt = c * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+      if (t == 0) {
+        m = mt;
+      } else if (__any_sync(0xffffffffu, mt > m + kRescale)) {
+        // the score MMA of this tile was issued behind the previous P V, so O is complete here
+        const float mn = fmaxf(m, mt);
+        const float f = ex2(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        l *= f;
+#pragma unroll 1
+        for (int ch = 0; ch < DH / 32; ++ch) {
+          float o[32];
+          tmem_ld32(tO + ch * 32, o);
+          tmem_ld_wait();
+          uint32_t u[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * f);
+          tmem_st16(tO + ch * 32, u);
+          tmem_st16(tO + ch * 32 + 16, u + 16);
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      const float2 nb = make_float2(-base, -base);
+      float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t u[16];
+        if (masked) {   // the polynomial does not reach 0, which hidden keys need
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = __ffma2_rn(make_float2(v[ch * 32 + 2 * j], v[ch * 32 + 2 * j + 1]), cc, nb);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            if (j & 1) s1 = __fadd2_rn(s1, e);
+            else s0 = __fadd2_rn(s0, e);
+            u[j] = pack_bf16x2(e.x, e.y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float* w = v + ch * 32 + 2 * j;
+            const float2 e0 = exp2_pair<0>(__ffma2_rn(make_float2(w[0], w[1]), cc, nb));
+            const float2 e1 = exp2_pair<1>(__ffma2_rn(make_float2(w[2], w[3]), cc, nb));
+            const float2 e2 = exp2_pair<2>(__ffma2_rn(make_float2(w[4], w[5]), cc, nb));
+            const float2 e3 = exp2_pair<3>(__ffma2_rn(make_float2(w[6], w[7]), cc, nb));
+            s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
+            s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
+            u[j] = pack_bf16x2(e0.x, e0.y);
+            u[j + 1] = pack_bf16x2(e1.x, e1.y);
+            u[j + 2] = pack_bf16x2(e2.x, e2.y);
+            u[j + 3] = pack_bf16x2(e3.x, e3.y);
+          }
+        }
+        tmem_st16(tS + ch * 16, u);
+      }
+      l += (s0.x + s1.x) + (s0.y + s1.y);
+      tmem_st_wait();
+      tc_before_sync();
+      mbar_arrive(&bars.p_ready[g]);
+    }
+    // rows that see nothing have l = 0 and O = 0; a NaN sum stays one
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    if (!aborted && my_T > 0 && !warp_wait(&bars.o_full[g], 0, abort_flag, wlim)) aborted = true;
+    if (!aborted) {
+      tc_after_sync();
+      const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH);
+#pragma unroll 1
+      for (int ch = 0; ch < DH / 32; ++ch) {
+        float o[32];
+        if (my_T > 0) {
+          tmem_ld32(tO + ch * 32, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+        }
+        if (r < my_rows) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                         pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        }
+      }
+      if (p.stat_m && r < my_rows) {
+        const int64_t at = static_cast<int64_t>(my_head) * a.total_q + row;
+        p.stat_m[at] = m == -INFINITY ? 0.0f : -m;
+        p.stat_l[at] = inv;
+      }
+    }
+  }
+  tc_before_sync();
+  const bool any_abort = __syncthreads_or(aborted);
+  if (any_abort && tid == 0) report(a.dev_status, SPATTEN_E_TIMEOUT);
+  if (warp == kMma) {
+    tc_after_sync();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+// =================================================================================================
+// WEIGHT
+// =================================================================================================
+template <int DH_>
+struct WeightCfg {
+  static constexpr int DH = DH_;
+  static constexpr int kStages = DH == 64 ? 3 : 2;
+  static constexpr uint32_t kTile = kKT * DH * 2u;
+  static constexpr uint32_t kSmem = (1 + kStages) * kTile + 1024u;
+  static constexpr int kSoftmax = 256, kThreads = kSoftmax + 64;
+  static constexpr uint32_t kTmem = 256;   // two score buffers
+};
+
+template <int NST>
+struct WeightBars {
+  uint64_t k_full, q_full[NST], q_empty[NST], s_full[2], s_empty[2], drain;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
+  constexpr int DH = C::DH, NST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ WeightBars<NST> bars;
+  __shared__ __align__(16) float stat_m[NST][kKT], stat_l[NST][kKT];
+  __shared__ float half_sum[kKT];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const spatten_prompt_args& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // tiles from the front: early keys are seen by the most rows
+  const SeqTile st = find_seq_tile<true>(a.cu_kv, a.B, a.total_kv, kKT, blockIdx.x / a.H);
+  if (st.b < 0) return;
+  const int h = blockIdx.x % a.H, G = a.H / a.H_kv, hk = h / G;
+  const PackedRows qr = packed_rows(a.cu_q, st.b, a.total_q), kr = packed_rows(a.cu_kv, st.b, a.total_kv);
+  const int j0 = st.tile * static_cast<int>(kKT), shift = kr.n - qr.n;
+  const int rt0 = max(0, j0 - shift) / static_cast<int>(kKT);   // the first row tile that sees key j0
+  const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
+
+  constexpr int kProducer = 8, kMma = 9;
+  if (warp == kMma) tmem_alloc(&tmem_base, C::kTmem);
+  if (tid == 0) {
+    abort_word = 0;
+    mbar_init(&bars.k_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&bars.q_full[s], 33);
+      mbar_init(&bars.q_empty[s], 9);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.s_empty[s], 8);
+    }
+    mbar_init(&bars.drain, 1);
+    fence_mbar_init();
+  }
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = tmem_base, wlim = p.wait_limit;
+  bool aborted = false;
+  float total = 0.0f;
+
+  if (warp == kProducer) {
+    int issued = 0;
+    if (lane == 0 && NT > 0) {
+      mbar_arrive_expect_tx(&bars.k_full, C::kTile);
+      load_tile<DH>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
+    }
+    const int64_t at = static_cast<int64_t>(h) * a.total_q + qr.first;
+    for (int t = 0; t < NT; ++t) {
+      const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
+      float sm[4], sl[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // rows past the sequence are masked where they are used
+        const int i = i0 + lane + 32 * k;
+        sm[k] = i < qr.n ? p.stat_m[at + i] : 0.0f;
+        sl[k] = i < qr.n ? p.stat_l[at + i] : 0.0f;
+      }
+      if (!warp_wait(&bars.q_empty[s], ((t / NST) & 1) ^ 1u, abort_flag, wlim)) {
+        aborted = true;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars.q_full[s], C::kTile);
+        load_tile<DH>(smem + (1 + s) * C::kTile, &maps.q, h, qr.first + i0, &bars.q_full[s]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        stat_m[s][lane + 32 * k] = sm[k];
+        stat_l[s][lane + 32 * k] = sl[k];
+      }
+      mbar_arrive(&bars.q_full[s]);
+      ++issued;
+    }
+    __syncwarp();
+    if (aborted && lane == 0) {
+      drain_wait(&bars.k_full, 0);
+      for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.q_full[x % NST], (x / NST) & 1);
+    }
+  } else if (warp == kMma) {
+    if (lane == 0 && NT > 0) {
+      const uint32_t sK = smem_u32(smem);
+      if (!wait_bar(&bars.k_full, 0, abort_flag, wlim)) aborted = true;
+      for (int t = 0; t < NT && !aborted; ++t) {
+        const int s = t % NST;
+        if (!wait_bar(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
+            !wait_bar(&bars.s_empty[t & 1], ((t >> 1) & 1) ^ 1u, abort_flag, wlim)) {
+          aborted = true;
+          break;
+        }
+        tc_after_sync();
+        mma_scores<DH>(tmem + (t & 1) * 128, sK, sK + (1 + s) * C::kTile);
+        mma_commit(&bars.s_full[t & 1]);
+        mma_commit(&bars.q_empty[s]);
+      }
+      if (aborted) {
+        mma_commit(&bars.drain);
+        drain_wait(&bars.drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int half = warp >> 2, col0 = half * 64;
+    const int j = j0 + (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const float c = a.sm_scale * kLog2e;
+    const float2 cc = make_float2(c, c);
+    for (int t = 0; t < NT; ++t) {
+      const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
+      if (!warp_wait(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
+          !warp_wait(&bars.s_full[t & 1], (t >> 1) & 1, abort_flag, wlim)) {
+        aborted = true;
+        break;
+      }
+      tc_after_sync();
+      float v[64];
+      tmem_ld32(tmem + lanes + (t & 1) * 128 + col0, v);
+      tmem_ld32(tmem + lanes + (t & 1) * 128 + col0 + 32, v + 32);
+      tmem_ld_wait();
+      tc_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
+      const float4* sm = reinterpret_cast<const float4*>(&stat_m[s][col0]);
+      const float4* sl = reinterpret_cast<const float4*>(&stat_l[s][col0]);
+      float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+      if (i0 + static_cast<int>(kKT) <= qr.n && j0 + static_cast<int>(kKT) - 1 <= i0 + shift) {
+#pragma unroll
+        for (int q = 0; q < 16; q += 2) {
+          const float4 m0 = sm[q], l0 = sl[q], m1 = sm[q + 1], l1 = sl[q + 1];
+          const float* w = v + 4 * q;
+          s0 = __ffma2_rn(exp2_pair<0>(__ffma2_rn(make_float2(w[0], w[1]), cc, make_float2(m0.x, m0.y))), make_float2(l0.x, l0.y), s0);
+          s1 = __ffma2_rn(exp2_pair<1>(__ffma2_rn(make_float2(w[2], w[3]), cc, make_float2(m0.z, m0.w))), make_float2(l0.z, l0.w), s1);
+          s0 = __ffma2_rn(exp2_pair<2>(__ffma2_rn(make_float2(w[4], w[5]), cc, make_float2(m1.x, m1.y))), make_float2(l1.x, l1.y), s0);
+          s1 = __ffma2_rn(exp2_pair<3>(__ffma2_rn(make_float2(w[6], w[7]), cc, make_float2(m1.z, m1.w))), make_float2(l1.z, l1.w), s1);
+        }
+      } else {
+        const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float4 m0 = sm[q], l0 = sl[q];
+          const float mm[4] = {m0.x, m0.y, m0.z, m0.w}, ll[4] = {l0.x, l0.y, l0.z, l0.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int col = 4 * q + k;
+            const float e = ex2(fmaf(v[col], c, mm[k])) * ll[k];
+            const float w = col >= lo && col < hi ? e : 0.0f;
+            if (k & 1) s1.x += w;
+            else s0.x += w;
+          }
+        }
+      }
+      total += (s0.x + s1.x) + (s0.y + s1.y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_empty[s]);
+    }
+    if (half) half_sum[(warp & 3) * 32 + lane] = total;
+  }
+  tc_before_sync();
+  const bool any_abort = __syncthreads_or(aborted);
+  if (any_abort && tid == 0) report(a.dev_status, SPATTEN_E_TIMEOUT);
+  if (tid < static_cast<int>(kKT) && j0 + tid < kr.n) {
+    const float sum = any_abort ? 0.0f : total + half_sum[tid];
+    const int j = j0 + tid;
+    if (G > 1) {
+      p.part[static_cast<int64_t>(h) * a.total_kv + kr.first + j] = sum;
+    } else if (j < a.weight_cap) {
+      a.weight[static_cast<int64_t>(st.b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
+    } else {
+      report(a.dev_status, SPATTEN_E_INDEX);
+    }
+  }
+  if (warp == kMma) {
+    tc_after_sync();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+// weight += the sums of a group's heads, in head order; blockIdx.y = key/value head
+__global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem p) {
+  const spatten_prompt_args& a = p.a;
+  const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
+  if (r >= a.total_kv) return;
+  const int b = owner_of_row(a.cu_kv, a.B, r);
+  if (b < 0) return;
+  const PackedRows kr = packed_rows(a.cu_kv, b, a.total_kv);
+  const int j = r - kr.first;
+  if (kr.bad || j < 0 || j >= kr.n) return;
+  if (j >= a.weight_cap) {
+    report(a.dev_status, SPATTEN_E_INDEX);
+    return;
+  }
+  const float* part = p.part + static_cast<int64_t>(hk) * G * a.total_kv + r;
+  float sum = 0.0f;
+  for (int g = 0; g < G; ++g) sum += part[static_cast<int64_t>(g) * a.total_kv];
+  a.weight[static_cast<int64_t>(b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
+}
+
+// =================================================================================================
+// host
+// =================================================================================================
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// [rows][heads][DH] with a row stride of ld elements, read in boxes of 128 rows x 1 head x 64 channels
+int32_t make_map(CUtensorMap* m, const void* base, int dh, int heads, int rows, int64_t ld) {
+  const EncodeFn enc = encode_fn();
+  if (!enc) return SPATTEN_E_UNSUPPORTED;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dh) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, 1, kKT}, step[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPATTEN_OK : SPATTEN_E_UNSUPPORTED;
+}
+
+template <class O, class W>
+int32_t launch(const PromptProblem& p, cudaStream_t st) {
+  static DeviceOnce once;
+  int dev;
+  SPT_TRY(once_per_device(once, &dev, [](int) -> int32_t {
+    SPT_CUDA(cudaFuncSetAttribute(prompt_out_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, O::kSmem));
+    SPT_CUDA(cudaFuncSetAttribute(prompt_weight_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem));
+    return SPATTEN_OK;
+  }));
+  const spatten_prompt_args& a = p.a;
+  Maps maps;
+  SPT_TRY(make_map(&maps.q, a.q, O::DH, a.H, a.total_q, a.q_ld_tok));
+  SPT_TRY(make_map(&maps.k, a.k, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
+  SPT_TRY(make_map(&maps.v, a.v, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
+  const bool pair_heads = O::NQ == 2 && (a.H / a.H_kv) % 2 == 0;
+  const int tile_rows = O::NQ == 2 && !pair_heads ? 256 : 128;
+  // a sequence's rows end in at most one partial tile, so this many tiles cover any offsets
+  const int64_t q_blocks = (static_cast<int64_t>(a.total_q) / tile_rows + a.B) * (pair_heads ? a.H / 2 : a.H);
+  const int64_t k_blocks = (static_cast<int64_t>(a.total_kv) / kKT + a.B) * a.H;
+  if (q_blocks > INT32_MAX || k_blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
+  prompt_out_kernel<O><<<static_cast<unsigned>(q_blocks), O::kThreads, O::kSmem, st>>>(p, maps);
+  SPT_TRY(launch_status());
+  if (!a.weight) return SPATTEN_OK;
+  prompt_weight_kernel<W><<<static_cast<unsigned>(k_blocks), W::kThreads, W::kSmem, st>>>(p, maps);
+  SPT_TRY(launch_status());
+  if (a.H == a.H_kv) return SPATTEN_OK;
+  prompt_weight_reduce_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.total_kv, 256)), a.H_kv), 256, 0, st>>>(p);
+  return launch_status();
+}
+
+}  // namespace
+
+bool prompt_tc_supported(const spatten_prompt_args& a) {
+  // a tensor map holds row strides below 2^40 bytes
+  return a.dtype == SPATTEN_BF16 && a.total_kv > 0 && a.q_ld_tok < (1LL << 38) && a.kv_ld_tok < (1LL << 38);
+}
+
+int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st) {
+  if (p.a.d_h == 64) return launch<OutCfg<64, 1>, WeightCfg<64>>(p, st);
+  return launch<OutCfg<128, 2>, WeightCfg<128>>(p, st);
+}
+
+}  // namespace spt

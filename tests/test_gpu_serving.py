@@ -557,3 +557,19 @@ def test_generation_with_eviction(cuda, dtype, d, H, Hk):
     spread, _ = R.prompt_attention(host(q), kk, np.abs(vv), cu2, cu_kv, 1)
     check_out(host(o), ref, spread, score_step(host(q), kk, 70), dtype, pr, "second turn")
     assert st.seen.tolist() == [lens[b] + 13 + new[b] for b in range(B)] and int(st.status.item()) == 0
+
+
+@pytest.mark.parametrize("d,H", [(64, 2), (128, 4)])
+def test_prompt_forced_timeout_reports_status_and_context_survives(cuda, d, H):
+    """One poll per wait: the kernels give up, say so, and the next call is whole."""
+    S = lib()
+    p = Prompt(S, BF, d, H, 2, [600, 90], [700, 90], seed=21)
+    try:
+        S.set_wait_limit(1)
+        p.run()
+        assert int(p.status.item()) == S.E_TIMEOUT
+    finally:
+        S.set_wait_limit(0)
+    p.status.zero_()
+    p.w.copy_(p.w0)
+    p.run().check(UBF)
