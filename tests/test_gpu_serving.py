@@ -573,3 +573,23 @@ def test_prompt_forced_timeout_reports_status_and_context_survives(cuda, d, H):
     p.status.zero_()
     p.w.copy_(p.w0)
     p.run().check(UBF)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (F32, 128)])
+def test_attention_scores_in_the_workspace(cuda, dtype, d):
+    """Sixteen heads over 20,000 keys: the scores do not fit the SMs' shared memory."""
+    S = lib()
+    n = [20000]
+    c = Cache(S, 1, 1, d, n[0], seed=31)
+    q = torch.randn((1, 16, d), device="cuda").to(dtype)
+    a = S.make_kv4_attn_args(c.c, q, torch.empty_like(q), i32(n), n[0])
+    assert S.kv4_attention_workspace_size(a) >= 16 * n[0] * 4
+    w0 = c.t["weight"].clone()
+    o, status = run_attention(S, c, q, n)
+    assert status == 0
+    k, v = c.values()
+    ref, w = R.kv4_attention(host(q)[0], k[0], v[0], n[0])
+    spread, _ = R.kv4_attention(host(q)[0], k[0], np.abs(v[0]), n[0])
+    e = score_step(host(q)[0], k[0], n[0])
+    check_out(host(o)[0], ref, spread, e, dtype, UBF if dtype == BF else 2 * U32)
+    check_weight(host(c.t["weight"])[0], host(w0)[0], w, e)
