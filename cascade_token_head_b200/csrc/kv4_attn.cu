@@ -33,16 +33,16 @@ namespace spt {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
-constexpr int kStages = 4;             // tiles in a warp's ring
+constexpr int kStages = 3;             // tiles in a warp's ring (4 leave room for less scores)
 constexpr int kStageBytes = 2304;      // 1024 + 1024 bytes of codes, 128 + 128 of scales
 constexpr int kMaxHeads = 16;          // heads of a group per pass over the keys
+constexpr int kMaxC = 8;               // CTAs per cluster
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;       // growth of a maximum (log2) that makes the sums be rescaled
-constexpr int kRing = kWarps * kStages * kStageBytes;
-
-// shared memory left for scores: with two CTAs on an SM, and with one (an SM has 228 KB, 1 KB of it per
-// CTA reserved; the CTA's other arrays take up to 10 KB)
-constexpr size_t kSharedTwo = 227 * 1024 / 2 - kRing - 11 * 1024, kSharedOne = 227 * 1024 - kRing - 11 * 1024;
+// the warps' rings, which later hold their output sums
+__host__ __device__ constexpr int ring_bytes(int dh, int nh) {
+  return kWarps * (kStages * kStageBytes > nh * 8 * dh * 4 ? kStages * kStageBytes : nh * 8 * dh * 4);
+}
 
 template <int DH> constexpr int kTileKeys = 2048 / DH;
 
@@ -55,18 +55,37 @@ struct AttnArgs {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool ok) {
-  const int n = ok ? BYTES : 0;   // 0 bytes read: the destination is zero-filled
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+// copies, or zero-fills; `valid` is an address that may be read in either case
+template <int BYTES>
+__device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, const void* valid, bool ok) {
+  const void* p = ok ? src : valid;
+  const int n = ok ? BYTES : 0;
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(p), "n"(BYTES), "r"(n) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16_zero(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -99,9 +118,9 @@ __device__ __forceinline__ float ex2(float x) {
 // two nibbles (bits 0-3 and 16-19 of w) as the bfloat16 pair of their codes
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   const uint32_t u = (w & 0x000f000fu) | 0x43004300u;   // 128 + u: exact in bfloat16's 8 bits
-  const __nv_bfloat162 off = __halves2bfloat162(__float2bfloat16_rn(-136.0f), __float2bfloat16_rn(-136.0f));
-  const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&u), off);
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0xc308c308u));   // - 136
+  return r;
 }
 
 // Where row r of a tile of V codes lies in its stage: with the rows of a quad's four lanes (2t, or
@@ -121,62 +140,96 @@ struct Warp {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kQ = kF32 ? 2 : 1;   // terms of a query
   static constexpr int kP = kF32 ? 3 : 1;   // terms of a P'
-  uint32_t q[NH][kQ][G32][2][2];            // B operand of the scores
-  float start[NH][G32][2], scale[NH][2];    // accumulators' start, factor to log2 units (heads 2t, 2t + 1)
+  // what the lanes need of one column of heads, made once per CTA
+  struct Query {
+    uint4 q[kQ][G32][32];         // B operand of the scores: (step, half) of a group
+    uint2 start[32];              // B operand of the scores' start
+    float2 scale[32];             // factor to log2 units
+  };
+  uint32_t q[NH][kQ][G32][4];
+  uint32_t start[NH][2];
+  float scale[NH][2];
   float o[NH][DH / 16][4];
-  float m[NH][2], nb[NH][2], l[NH][2];      // maximum, what the exponents add (-m, or 0), sum of this lane's keys
+  float lim[NH][2], nb[NH][2], l[NH][2];    // maximum + kRescale, what the exponents add (-maximum, or 0), sum of this lane's keys
 
-  // heads h0 .. of query row qrow (heads past `heads` are zeros)
-  __device__ __forceinline__ void init(const T* qrow, int heads, float sm_scale, int lane) {
-    const int gid = lane >> 2, t = lane & 3;
+  // column nh: heads h0 + 8 nh .. of query row qrow (heads past `heads` are zeros); one warp
+  static __device__ __forceinline__ void prepare(Query& out, const T* qrow, int nh, int heads, float sm_scale, int lane) {
+    const int gid = lane >> 2, t = lane & 3, h = nh * 8 + gid;
+    float f[G32][8], start[G32], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < G32; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
+      if (h < heads) load8(qrow + static_cast<int64_t>(h) * DH + 32 * j + 8 * t, f[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[j][i]));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^E q has its maximum in [2^13, 2^14); E stays where 2^E and 2^(12 - E) are normal numbers
+    const int E = max(-114, min(126, 13 + 127 - static_cast<int>(__float_as_uint(amax) >> 23)));
+    const float up = __uint_as_float(static_cast<uint32_t>(E + 127) << 23);
+    const float sc = sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(12 - E + 127) << 23);
+#pragma unroll
+    for (int j = 0; j < G32; ++j) {
+      float sum = 0.0f;
+      uint32_t u[kQ][4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {   // channels c, c + 4 of the word; the odd ones against 16 u
+        const float w = (c & 1) ? 0.0625f : 1.0f;
+        float x = f[j][c] * up * w, y = f[j][c + 4] * up * w;
+#pragma unroll
+        for (int e = 0; e < kQ; ++e) {
+          u[e][c] = pack_half(x, y);
+          const float2 r = half_pair(u[e][c]);
+          sum += (r.x + r.y) * ((c & 1) ? 16.0f : 1.0f);
+          x -= r.x;
+          y -= r.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kQ; ++e) out.q[e][j][lane] = make_uint4(u[e][0], u[e][1], u[e][2], u[e][3]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      start[j] = sum * (-8.0f * 5.9604644775390625e-08f);   // -8 2^-24
+    }
+    // -8 sum(q) of the groups as three bfloat16 each, along the operand's 16 rows against the keys' scales:
+    // rows 2t, 2t + 1 hold a term of two groups (128 channels: t = 0, 1 the first, 2, 3 the second, 0, 1 of
+    // the upper eight the third; 64: t = 0, 1, 2)
+    uint32_t term[3][G32 / 2];
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+#pragma unroll
+      for (int j = 0; j < G32 / 2; ++j) {
+        term[e][j] = pack_bf16(start[2 * j], start[2 * j + 1]);
+        start[2 * j] -= bf_lo(term[e][j]);
+        start[2 * j + 1] -= bf_hi(term[e][j]);
+      }
+    if constexpr (DH == 128)
+      out.start[lane] = make_uint2((t & 1) ? term[t >> 1][1] : term[t >> 1][0], t > 1 ? 0u : term[2][t & 1]);
+    else
+      out.start[lane] = make_uint2(t == 3 ? 0u : term[t][0], 0u);
+    out.scale[lane] = make_float2(__shfl_sync(0xffffffffu, sc, 8 * t), __shfl_sync(0xffffffffu, sc, 8 * t + 4));
+  }
+
+  __device__ __forceinline__ void init(const Query* in, int lane) {
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      const int h = nh * 8 + gid;
-      float f[G32][8], amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < G32; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
-        if (h < heads) load8(qrow + static_cast<int64_t>(h) * DH + 32 * j + 8 * t, f[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[j][i]));
+        for (int e = 0; e < kQ; ++e) {
+          const uint4 u = in[nh].q[e][j][lane];
+          q[nh][e][j][0] = u.x, q[nh][e][j][1] = u.y, q[nh][e][j][2] = u.z, q[nh][e][j][3] = u.w;
+        }
       }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^E q has its maximum in [2^13, 2^14); E stays where 2^E and 2^(12 - E) are normal numbers
-      const int E = max(-114, min(126, 13 + 127 - static_cast<int>(__float_as_uint(amax) >> 23)));
-      const float up = __uint_as_float(static_cast<uint32_t>(E + 127) << 23);
-      const float sc = sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(12 - E + 127) << 23);
-#pragma unroll
-      for (int j = 0; j < G32; ++j) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {   // channels c, c + 4 of the word; the odd ones against 16 u
-            const int c = 2 * s + k;
-            const float w = k ? 0.0625f : 1.0f;
-            float a = f[j][c] * up * w, b = f[j][c + 4] * up * w;
-#pragma unroll
-            for (int e = 0; e < kQ; ++e) {
-              const uint32_t u = pack_half(a, b);
-              const float2 r = half_pair(u);
-              q[nh][e][j][s][k] = u;
-              sum += (r.x + r.y) * (k ? 16.0f : 1.0f);
-              a -= r.x;
-              b -= r.y;
-            }
-          }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -8.0f * 5.9604644775390625e-08f;   // -8 2^-24
-#pragma unroll
-        for (int c = 0; c < 2; ++c) start[nh][j][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4);
-      }
+      const uint2 st = in[nh].start[lane];
+      start[nh][0] = st.x, start[nh][1] = st.y;
+      const float2 sc = in[nh].scale[lane];
+      scale[nh][0] = sc.x, scale[nh][1] = sc.y;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        scale[nh][c] = __shfl_sync(0xffffffffu, sc, (2 * t + c) * 4);
-        m[nh][c] = -INFINITY;
+        lim[nh][c] = -INFINITY;
         nb[nh][c] = l[nh][c] = 0.0f;
       }
 #pragma unroll
@@ -185,37 +238,39 @@ struct Warp {
         for (int k = 0; k < 4; ++k) o[nh][i][k] = 0.0f;
     }
   }
+  __device__ __forceinline__ float maximum(int nh, int c) const { return lim[nh][c] == -INFINITY ? -INFINITY : -nb[nh][c]; }
 
-  // keys 16 sub .. + 15 of the staged tile, key0 the first one's index in the CTA's run, n its keys
-  __device__ __forceinline__ void tile16(const uint8_t* st, int sub, int key0, int n, float* x, int x_ld, int heads, int lane) {
-    const int gid = lane >> 2, t = lane & 3;
-    const uint8_t *sk = st, *sv = st + 1024, *sks = st + 2048, *svs = st + 2176;
-    const int r0 = sub * 16 + gid, r1 = r0 + 8;
-    // scores
+  // sixteen keys of a staged tile; sk, sv, ss: this lane's first K and V codes and K scales of them.
+  // xs: where this lane's scores go (keys gid and gid + 8 of heads 2t and, x_ld behind, 2t + 1; 8 x_ld per
+  // column), or NULL.  left: keys there are, counted from key gid (FULL: all).
+  template <bool FULL>
+  __device__ __forceinline__ void tile16(const uint8_t* sk, const uint8_t* sv, const uint8_t* ss, float* xs, int x_ld, int heads,
+                                         int left, int lane) {
+    const int t = lane & 3;
     uint32_t kw[2][G32], ks[2][G32 / 2], vs[2][G32 / 2];
-    if constexpr (DH == 128) {
-      const uint4 a = *reinterpret_cast<const uint4*>(sk + r0 * 64 + t * 16), b = *reinterpret_cast<const uint4*>(sk + r1 * 64 + t * 16);
-      kw[0][0] = a.x, kw[0][1] = a.y, kw[0][2] = a.z, kw[0][3] = a.w;
-      kw[1][0] = b.x, kw[1][1] = b.y, kw[1][2] = b.z, kw[1][3] = b.w;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint2 c = *reinterpret_cast<const uint2*>(sks + (r ? r1 : r0) * 8), d = *reinterpret_cast<const uint2*>(svs + (r ? r1 : r0) * 8);
+    for (int r = 0; r < 2; ++r) {   // keys gid, gid + 8
+      if constexpr (DH == 128) {
+        const uint4 k = *reinterpret_cast<const uint4*>(sk + r * 512);
+        kw[r][0] = k.x, kw[r][1] = k.y, kw[r][2] = k.z, kw[r][3] = k.w;
+        const uint2 c = *reinterpret_cast<const uint2*>(ss + r * 64), d = *reinterpret_cast<const uint2*>(ss + 128 + r * 64);
         ks[r][0] = c.x, ks[r][1] = c.y, vs[r][0] = d.x, vs[r][1] = d.y;
-      }
-    } else {
-      const uint2 a = *reinterpret_cast<const uint2*>(sk + r0 * 32 + t * 8), b = *reinterpret_cast<const uint2*>(sk + r1 * 32 + t * 8);
-      kw[0][0] = a.x, kw[0][1] = a.y, kw[1][0] = b.x, kw[1][1] = b.y;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ks[r][0] = *reinterpret_cast<const uint32_t*>(sks + (r ? r1 : r0) * 4);
-        vs[r][0] = *reinterpret_cast<const uint32_t*>(svs + (r ? r1 : r0) * 4);
+      } else {
+        const uint2 k = *reinterpret_cast<const uint2*>(sk + r * 256);
+        kw[r][0] = k.x, kw[r][1] = k.y;
+        ks[r][0] = *reinterpret_cast<const uint32_t*>(ss + r * 32);
+        vs[r][0] = *reinterpret_cast<const uint32_t*>(ss + 128 + r * 32);
       }
     }
     float s[NH][4];
+    {
+      // 128 channels: scales 0, 1 on even, 2, 3 on odd lanes of a quad
+      const uint8_t* sa = DH == 128 ? ss + (t & 1) * 4 : ss;
+      const uint32_t k0 = *reinterpret_cast<const uint32_t*>(sa), k1 = *reinterpret_cast<const uint32_t*>(sa + (DH == 128 ? 64 : 32));
+      const uint32_t ak[4] = {k0, k1, k0, k1};
 #pragma unroll
-    for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[nh][k] = 0.0f;
+      for (int nh = 0; nh < NH; ++nh) mma_bf16_zero(s[nh], ak, start[nh][0], start[nh][1]);
+    }
 #pragma unroll
     for (int j = 0; j < G32; ++j) {
       const uint32_t w0 = kw[0][j], w1 = kw[1][j], v0 = w0 >> 8, v1 = w1 >> 8;
@@ -225,37 +280,36 @@ struct Warp {
       const float f1 = (j & 1) ? bf_hi(ks[1][j >> 1]) : bf_lo(ks[1][j >> 1]);
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
-        float c[4] = {start[nh][j][0], start[nh][j][1], start[nh][j][0], start[nh][j][1]};
+        float c[4];
 #pragma unroll
         for (int e = 0; e < kQ; ++e) {
-          mma_f16(c, a0, q[nh][e][j][0][0], q[nh][e][j][0][1]);
-          mma_f16(c, a1, q[nh][e][j][1][0], q[nh][e][j][1][1]);
+          if (e == 0) mma_f16_zero(c, a0, q[nh][e][j][0], q[nh][e][j][1]);
+          else mma_f16(c, a0, q[nh][e][j][0], q[nh][e][j][1]);
+          mma_f16(c, a1, q[nh][e][j][2], q[nh][e][j][3]);
         }
-        s[nh][0] = fmaf(f0, c[0], s[nh][0]);
-        s[nh][1] = fmaf(f0, c[1], s[nh][1]);
-        s[nh][2] = fmaf(f1, c[2], s[nh][2]);
-        s[nh][3] = fmaf(f1, c[3], s[nh][3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[nh][k] = fmaf(k < 2 ? f0 : f1, c[k], s[nh][k]);
       }
     }
-    const int i0 = key0 + r0, i1 = key0 + r1;
     bool grown = false;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float y = (s[nh][k] * 4096.0f) * scale[nh][k & 1];   // 2^24 in two factors that stay in range
-        s[nh][k] = (k < 2 ? i0 : i1) < n ? y : -INFINITY;
-        grown |= s[nh][k] > m[nh][k & 1] + kRescale;
+        s[nh][k] = (s[nh][k] * 4096.0f) * scale[nh][k & 1];   // 2^24 in two factors that stay in range
+        if (!FULL && left <= (k < 2 ? 0 : 8)) s[nh][k] = -INFINITY;
+        grown |= s[nh][k] > lim[nh][k & 1];
       }
-      if (x) {
+      if (xs) {
+        float* p = xs + nh * 8 * x_ld;
         const int h = nh * 8 + 2 * t;
         if (h < heads) {
-          if (i0 < n) x[h * x_ld + i0] = s[nh][0];
-          if (i1 < n) x[h * x_ld + i1] = s[nh][2];
+          if (FULL || left > 0) p[0] = s[nh][0];
+          if (FULL || left > 8) p[8] = s[nh][2];
         }
         if (h + 1 < heads) {
-          if (i0 < n) x[(h + 1) * x_ld + i0] = s[nh][1];
-          if (i1 < n) x[(h + 1) * x_ld + i1] = s[nh][3];
+          if (FULL || left > 0) p[x_ld] = s[nh][1];
+          if (FULL || left > 8) p[x_ld + 8] = s[nh][3];
         }
       }
     }
@@ -267,10 +321,11 @@ struct Warp {
           float mx = fmaxf(s[nh][c], s[nh][c + 2]);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-          mx = fmaxf(mx, m[nh][c]);
+          const float old = maximum(nh, c);
+          mx = fmaxf(mx, old);
+          lim[nh][c] = mx + kRescale;
           nb[nh][c] = mx == -INFINITY ? 0.0f : -mx;
-          const float f = ex2(m[nh][c] + nb[nh][c]);
-          m[nh][c] = mx;
+          const float f = ex2(old + nb[nh][c]);
           l[nh][c] *= f;
 #pragma unroll
           for (int i = 0; i < DH / 16; ++i) {
@@ -290,15 +345,12 @@ struct Warp {
     uint32_t vw[2][G32];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int ra = sub * 16 + half * 8 + 2 * t;
       if constexpr (DH == 128) {
-        const uint2 a = *reinterpret_cast<const uint2*>(sv + v_offset<DH>(ra, gid * 8));
-        const uint2 b = *reinterpret_cast<const uint2*>(sv + v_offset<DH>(ra + 1, gid * 8));
+        const uint2 a = *reinterpret_cast<const uint2*>(sv + half * 512), b = *reinterpret_cast<const uint2*>(sv + half * 512 + 256);
         vw[half][0] = __byte_perm(a.x, b.x, 0x5410), vw[half][1] = __byte_perm(a.x, b.x, 0x7632);
         vw[half][2] = __byte_perm(a.y, b.y, 0x5410), vw[half][3] = __byte_perm(a.y, b.y, 0x7632);
       } else {
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(sv + v_offset<DH>(ra, gid * 4));
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(sv + v_offset<DH>(ra + 1, gid * 4));
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(sv + half * 256), b = *reinterpret_cast<const uint32_t*>(sv + half * 256 + 128);
         vw[half][0] = __byte_perm(a, b, 0x5410), vw[half][1] = __byte_perm(a, b, 0x7632);
       }
     }
@@ -340,14 +392,18 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   using W = Warp<DH, NH, T>;
   constexpr int TK = W::TK, G32 = W::G32, kHeads = NH * 8;
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings (later their sums), then the scores
+  __shared__ __align__(16) typename W::Query query[NH];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-  __shared__ float c_m[kHeads], c_l[kHeads], f_m[kHeads], f_l[kHeads];   // the CTA's, the cluster's (sum inverted)
-  __shared__ float c_o[kHeads][DH];
+  // what the CTAs of the cluster send: maxima and sums, and their share of the outputs this CTA adds up
+  __shared__ float2 in_ml[kMaxC][kHeads];
+  __shared__ float in_o[kHeads * DH];
+  __shared__ float2 f[kHeads];                   // the cluster's maxima, and sums inverted
   cg::cluster_group cluster = cg::this_cluster();
   const int C = gridDim.x, rank = blockIdx.x;
   const spatten_kv4_attn_args& a = args.a;
   const spatten_kv4_cache& c = a.cache;
   const int hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gid = lane >> 2, t = lane & 3;
   const int group = a.H / c.H_kv;
   const int n_all = clamp_len(a.len[b], a.n_max, a.dev_status);
   const int run = (((n_all + C - 1) / C) + TK - 1) / TK * TK;   // keys per CTA
@@ -355,55 +411,92 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   const int64_t row0 = (static_cast<int64_t>(b) * c.H_kv + hk) * c.cap + first;
   const int tiles = (n + TK - 1) / TK;
   uint8_t* ring = smem + warp * kStages * kStageBytes;
-  float* x = args.x ? args.x + ((static_cast<int64_t>(b) * c.H_kv + hk) * C + rank) * args.heads * static_cast<int64_t>(args.x_ld)
-                    : reinterpret_cast<float*>(smem + kRing);
+  const int x_ld = args.x_ld;
+  float* x = args.x ? args.x + ((static_cast<int64_t>(b) * c.H_kv + hk) * C + rank) * args.heads * static_cast<int64_t>(x_ld)
+                    : reinterpret_cast<float*>(smem + ring_bytes(DH, NH));
   if (!a.update_weight) x = nullptr;
 
-  auto load = [&](int tile, int stage) {
-    const uint32_t dst = smem_addr(ring + stage * kStageBytes);
-    const int key0 = tile * TK;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = lane + 32 * i, r = e / (DH / 32), ch = e % (DH / 32);
-      const bool ok = key0 + r < n;
-      const int64_t at = (row0 + (ok ? key0 + r : 0)) * (DH / 2) + ch * 16;
-      cp_async<16>(dst + r * (DH / 2) + ch * 16, c.k_codes + at, ok);
-      cp_async<16>(dst + 1024 + v_offset<DH>(r, ch * 16), c.v_codes + at, ok);
-    }
-    if constexpr (DH == 128) {
-      const int r = lane & 15;
-      const bool ok = key0 + r < n;
-      cp_async<8>(dst + 2048 + lane * 8, (lane < 16 ? c.k_scale : c.v_scale) + (row0 + (ok ? key0 + r : 0)) * G32, ok);
-    } else {
-      const bool ok = key0 + lane < n;
-      const int64_t at = (row0 + (ok ? key0 + lane : 0)) * G32;
-      cp_async<4>(dst + 2048 + lane * 4, c.k_scale + at, ok);
-      cp_async<4>(dst + 2176 + lane * 4, c.v_scale + at, ok);
+  // this lane's share of a tile's copies: two pieces of 16 bytes of each tensor's codes, and scales
+  constexpr int kPieces = DH / 32;
+  const int r_a = lane / kPieces, ch = lane % kPieces;
+  const int64_t at0 = (row0 + warp * TK) * (DH / 2) + lane * 16;
+  const int64_t as0 = (row0 + warp * TK + (DH == 128 ? lane & 15 : lane)) * G32;
+  const uint16_t* gs0 = (DH == 64 || lane < 16 ? c.k_scale : c.v_scale) + as0;
+  const uint32_t d_code = smem_addr(ring) + lane * 16, d_v0 = smem_addr(ring) + 1024 + v_offset<DH>(r_a, ch * 16),
+                 d_v1 = smem_addr(ring) + 1024 + v_offset<DH>(r_a + 32 / kPieces, ch * 16),
+                 d_scale = smem_addr(ring) + 2048 + lane * (DH / 16);
+  // copies the warp's i-th tile
+  auto load = [&](int i, int stage) {
+    const uint32_t d = stage * kStageBytes;
+    const int64_t step = static_cast<int64_t>(i) * (kWarps * TK);
+    const uint8_t *pk = c.k_codes + at0 + step * (DH / 2), *pv = c.v_codes + at0 + step * (DH / 2);
+    const uint16_t* ps = gs0 + step * G32;
+    const int left = n - (i * kWarps + warp) * TK;
+    if (left >= TK) {
+      cp_async<16>(d_code + d, pk);
+      cp_async<16>(d_code + d + 512, pk + 512);
+      cp_async<16>(d_v0 + d, pv);
+      cp_async<16>(d_v1 + d, pv + 512);
+      if constexpr (DH == 128) {
+        cp_async<8>(d_scale + d, ps);
+      } else {
+        cp_async<4>(d_scale + d, ps);
+        cp_async<4>(d_scale + d + 128, c.v_scale + as0 + step * G32);
+      }
+    } else {   // rows past the keys are zero-filled, not read
+      const bool ok0 = r_a < left, ok1 = r_a + 32 / kPieces < left, oks = (DH == 128 ? lane & 15 : lane) < left;
+      cp_async_if<16>(d_code + d, pk, c.k_codes, ok0);
+      cp_async_if<16>(d_code + d + 512, pk + 512, c.k_codes, ok1);
+      cp_async_if<16>(d_v0 + d, pv, c.v_codes, ok0);
+      cp_async_if<16>(d_v1 + d, pv + 512, c.v_codes, ok1);
+      if constexpr (DH == 128) {
+        cp_async_if<8>(d_scale + d, ps, c.k_scale, oks);
+      } else {
+        cp_async_if<4>(d_scale + d, ps, c.k_scale, oks);
+        cp_async_if<4>(d_scale + d + 128, c.v_scale + as0 + step * G32, c.v_scale, oks);
+      }
     }
   };
+  // this lane's first codes and scales of a staged tile (slot t holds V's row 2t, slot 4 + t row 2t + 1)
+  const int lk = gid * (DH / 2) + t * (DH / 8), lv = 1024 + v_offset<DH>(2 * t, gid * (DH / 16)), ls = 2048 + gid * (DH / 16);
 
+  if (C > 1) cluster.barrier_arrive();   // this CTA runs: its shared memory can be written
   for (int h0 = 0; h0 < group; h0 += kHeads) {
     const int heads = min(kHeads, group - h0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (warp + kWarps * i < tiles) load(warp + kWarps * i, i);
+      if (warp + kWarps * i < tiles) load(i, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    if (warp < NH)
+      W::prepare(query[warp], static_cast<const T*>(a.q) + b * a.q_ld + (static_cast<int64_t>(hk) * group + h0) * DH, warp, heads,
+                 a.sm_scale, lane);
+    __syncthreads();
     W w;
-    w.init(static_cast<const T*>(a.q) + b * a.q_ld + (static_cast<int64_t>(hk) * group + h0) * DH, heads, a.sm_scale, lane);
+    w.init(query, lane);
+    float* xs = x ? x + 2 * t * x_ld + gid : nullptr;
     for (int tile = warp, i = 0; tile < tiles; tile += kWarps, ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();   // every lane's copies have landed, and every lane is done with the previous tile
-      if (tile + kWarps * (kStages - 1) < tiles) load(tile + kWarps * (kStages - 1), (i + kStages - 1) % kStages);
+      if (tile + kWarps * (kStages - 1) < tiles) load(i + kStages - 1, (i + kStages - 1) % kStages);
       asm volatile("cp.async.commit_group;" ::: "memory");
       const uint8_t* st = ring + (i % kStages) * kStageBytes;
+      const int key0 = tile * TK;
+      float* xt = xs ? xs + key0 : nullptr;
+      if (n - key0 >= TK) {
 #pragma unroll
-      for (int sub = 0; sub < TK / 16; ++sub) w.tile16(st, sub, tile * TK, n, x, args.x_ld, heads, lane);
+        for (int sub = 0; sub < TK / 16; ++sub)
+          w.template tile16<true>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads, 0, lane);
+      } else {
+#pragma unroll 1
+        for (int sub = 0; sub < TK / 16; ++sub)
+          w.template tile16<false>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads,
+                                   n - key0 - 16 * sub - gid, lane);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
     // the warps' sums, over their common maximum, in warp order
-    const int gid = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -412,71 +505,92 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         if (gid == 0) {
-          s_m[warp][nh * 8 + 2 * t + k] = w.m[nh][k];
+          s_m[warp][nh * 8 + 2 * t + k] = w.maximum(nh, k);
           s_l[warp][nh * 8 + 2 * t + k] = l;
         }
       }
-    __syncthreads();   // also: every ring is free
+    __syncthreads();   // also: every ring is free, and the query has been read
     float* part = reinterpret_cast<float*>(smem);   // [warp][head][channel]
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int h = nh * 8 + 2 * t + k;
-        float mx = s_m[0][h];
+        if (h < heads) {
+          float mx = s_m[0][h];
 #pragma unroll
-        for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][h]);
-        const float f = ex2(w.m[nh][k] - (mx == -INFINITY ? 0.0f : mx));
-        float* dst = part + (warp * kHeads + h) * DH;
+          for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][h]);
+          const float scale = ex2(w.maximum(nh, k) - (mx == -INFINITY ? 0.0f : mx));
+          float* dst = part + (warp * kHeads + h) * DH + 4 * gid;
 #pragma unroll
-        for (int j = 0; j < G32; ++j) {   // channels 32 j + 4 gid .. + 3
-          const float4 v = make_float4(w.o[nh][2 * j][k] * f, w.o[nh][2 * j][k + 2] * f, w.o[nh][2 * j + 1][k] * f,
-                                       w.o[nh][2 * j + 1][k + 2] * f);
-          if (h < heads) *reinterpret_cast<float4*>(dst + 32 * j + 4 * gid) = v;
+          for (int j = 0; j < G32; ++j)   // channels 32 j + 4 gid .. + 3
+            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(w.o[nh][2 * j][k] * scale, w.o[nh][2 * j][k + 2] * scale,
+                                                                   w.o[nh][2 * j + 1][k] * scale, w.o[nh][2 * j + 1][k + 2] * scale);
         }
       }
-    if (tid < heads) {
-      float mx = s_m[0][tid], l = 0.0f;
-      for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][tid]);
+    if (C > 1 && h0 == 0) cluster.barrier_wait();   // every CTA does
+    if (tid < heads * C) {   // the CTA's maxima and sums to every CTA
+      const int h = tid % heads;
+      float mx = s_m[0][h], l = 0.0f;
+#pragma unroll
+      for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][h]);
       const float base = mx == -INFINITY ? 0.0f : mx;
-      for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][tid], ex2(s_m[v][tid] - base), l);
-      c_m[tid] = mx;
-      c_l[tid] = l;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][h], ex2(s_m[v][h] - base), l);
+      *cluster.map_shared_rank(&in_ml[rank][h], tid / heads) = make_float2(mx, l);
     }
     __syncthreads();
+    const int share = heads * DH / C;   // the outputs that a CTA adds up
     for (int e = tid; e < heads * DH; e += kThreads) {
       float v = 0.0f;
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u) v += part[u * kHeads * DH + e];
-      c_o[e / DH][e % DH] = v;
+      for (int k = 0; k < kWarps; ++k) v += part[k * kHeads * DH + e];
+      const int to = e / share;
+      *cluster.map_shared_rank(&in_o[rank * share + (e - to * share)], to) = v;
     }
-    // the cluster's sums, in rank order
     if (C > 1) cluster.sync();
     else __syncthreads();
+    // the cluster's sums, in rank order
     if (tid < heads) {
       float mx = -INFINITY, l = 0.0f;
-      for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&c_m[tid], r));
+      for (int r = 0; r < C; ++r) mx = fmaxf(mx, in_ml[r][tid].x);
       const float base = mx == -INFINITY ? 0.0f : mx;
-      for (int r = 0; r < C; ++r) l = fmaf(*cluster.map_shared_rank(&c_l[tid], r), ex2(*cluster.map_shared_rank(&c_m[tid], r) - base), l);
-      f_m[tid] = base;
-      f_l[tid] = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // an empty sequence gives 0, NaN stays
+      for (int r = 0; r < C; ++r) l = fmaf(in_ml[r][tid].y, ex2(in_ml[r][tid].x - base), l);
+      f[tid] = make_float2(base, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));   // an empty sequence gives 0, NaN stays
     }
     __syncthreads();
-    for (int e = rank * kThreads + tid; e < heads * DH; e += C * kThreads) {
-      const int h = e / DH, ch = e % DH;
+    for (int e = tid; e < share; e += kThreads) {
+      const int h = (rank * share + e) / DH;
       float v = 0.0f;
-      for (int r = 0; r < C; ++r)
-        v = fmaf(*cluster.map_shared_rank(&c_o[h][ch], r), ex2(*cluster.map_shared_rank(&c_m[h], r) - f_m[h]), v);
-      st_from_float(static_cast<T*>(a.o) + b * a.o_ld + (static_cast<int64_t>(hk) * group + h0 + h) * DH + ch, v * f_l[h]);
+      for (int r = 0; r < C; ++r) v = fmaf(in_o[r * share + e], ex2(in_ml[r][h].x - f[h].x), v);
+      st_from_float(static_cast<T*>(a.o) + b * a.o_ld + (static_cast<int64_t>(hk) * group + h0) * DH + rank * share + e, v * f[h].y);
     }
-    if (x)
-      for (int i = tid; i < n; i += kThreads) {
-        float v = 0.0f;
-        for (int h = 0; h < heads; ++h) v = fmaf(ex2(x[h * args.x_ld + i] - f_m[h]), f_l[h], v);
-        c.weight[row0 + i] += v;
+    if (x) {
+      constexpr int kU = 4;   // rows in flight
+      for (int i0 = tid; i0 < n; i0 += kU * kThreads) {
+        float w0[kU], v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          w0[u] = i0 + u * kThreads < n ? c.weight[row0 + i0 + u * kThreads] : 0.0f;
+          v[u] = 0.0f;
+        }
+#pragma unroll 2
+        for (int h = 0; h < heads; ++h) {
+          const float2 fh = f[h];
+          const float* xh = x + h * x_ld + i0;
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (i0 + u * kThreads < n) v[u] = fmaf(ex2(xh[u * kThreads] - fh.x), fh.y, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (i0 + u * kThreads < n) c.weight[row0 + i0 + u * kThreads] = w0[u] + v[u];
       }
-    if (C > 1) cluster.sync();   // peers have read this CTA's sums
-    else __syncthreads();
+    }
+    if (h0 + kHeads < group) {   // the next heads' sums arrive once every CTA has read these
+      if (C > 1) cluster.sync();
+      else __syncthreads();
+    }
   }
 }
 
@@ -506,18 +620,22 @@ struct Shape {
 
 // Enough CTAs to fill the SMs, none with less than a tile per warp, and scores that let two CTAs share
 // an SM where more CTAs achieve that; scores that fit no SM go to the workspace.
+// (an SM has 228 KB, 1 KB of it per CTA reserved; a CTA's static arrays take up to 16 KB where two fit, else 20)
+constexpr size_t kSharedTwo = (113 - 16) * 1024, kSharedOne = (227 - 20) * 1024;   // ring and scores
+
 Shape shape(const spatten_kv4_attn_args& a) {
   Shape s{};
   const int tk = 2048 / a.cache.d_h;
   s.heads = std::min(a.H / a.cache.H_kv, kMaxHeads);
   const int64_t pairs = static_cast<int64_t>(a.cache.B) * a.cache.H_kv;
   auto ld = [&](int C) { return static_cast<int>(align_up(static_cast<size_t>(ceil_div(a.n_max, C)), 32) + 4); };
-  auto bytes = [&](int C) { return a.update_weight ? static_cast<size_t>(s.heads) * ld(C) * sizeof(float) : 0; };
+  const size_t ring = ring_bytes(a.cache.d_h, s.heads > 8 ? 2 : 1);
+  auto bytes = [&](int C) { return ring + (a.update_weight ? static_cast<size_t>(s.heads) * ld(C) * sizeof(float) : 0); };
   s.C = 1;
-  while (s.C < 8 && a.n_max > s.C * kWarps * tk && (pairs * s.C < sm_count() || bytes(s.C) > kSharedTwo)) s.C *= 2;
+  while (s.C < kMaxC && a.n_max > s.C * kWarps * tk && (pairs * s.C < sm_count() || bytes(s.C) > kSharedTwo)) s.C *= 2;
   s.x_ld = ld(s.C);
   s.x_ws = bytes(s.C) > kSharedOne;
-  s.x_smem = s.x_ws ? 0 : bytes(s.C);
+  s.x_smem = s.x_ws ? 0 : bytes(s.C) - ring;
   return s;
 }
 
@@ -535,7 +653,7 @@ int32_t launch(const AttnArgs& x, const Shape& s, cudaStream_t st) {
   int dev;
   SPT_TRY(once_per_device(once, &dev, [](int) -> int32_t {
     SPT_CUDA(cudaFuncSetAttribute(kv4_attn_kernel<DH, NH, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(kRing + kSharedOne)));
+                                  static_cast<int>(kSharedOne)));
     return SPATTEN_OK;
   }));
   cudaLaunchAttribute attr[1];
@@ -545,7 +663,7 @@ int32_t launch(const AttnArgs& x, const Shape& s, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(s.C), static_cast<unsigned>(x.a.cache.H_kv), static_cast<unsigned>(x.a.cache.B));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRing + s.x_smem;
+  cfg.dynamicSmemBytes = ring_bytes(DH, NH) + s.x_smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
