@@ -35,102 +35,139 @@ struct AppendArgs {
 };
 
 // Eight channels (one lane's share: a quarter of a 32-channel group) of one row to codes; the four
-// lanes of the group share their amax.  Returns the codes as nibbles (channel i at bits 4i) and the
-// scale's bfloat16 bits.
+// lanes of the group share their amax; whole warps call it.  Returns the codes as nibbles (channel i at
+// bits 4i) and the scale's bfloat16 bits.
+// The code is rint(x / s) of the IEEE quotient.  The product with an approximate reciprocal is off by less
+// than 2e-6 here, so its rounding is the quotient's unless it lies that near to a half; such lanes, and
+// subnormal scales (where the quotient may pass 7), divide.
 __device__ __forceinline__ uint32_t quantize8(float* x, uint32_t* scale_bits, bool* bad) {
-  float amax = 0.0f;
-  *bad = false;
+  float z = 0.0f, amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (!isfinite(x[i])) {
-      x[i] = 0.0f;
-      *bad = true;
-    }
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
+  for (int i = 0; i < 8; ++i) z = fmaf(x[i], 0.0f, z);   // NaN if any is not finite
+  *bad = z != 0.0f;
+  if (*bad)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = isfinite(x[i]) ? x[i] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
   if (__bfloat162float(sb) == 0.0f) sb = __float2bfloat16_rn(1.0f);
   const float s = __bfloat162float(sb);
   *scale_bits = __bfloat16_as_ushort(sb);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  constexpr float kRound = 12582912.0f + 8.0f;   // 1.5 * 2^23 + 8: the sum's low bits are rint(x / s) + 8
   uint32_t w = 0;
+  float off = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // the scale is rounded to nearest, so the largest quotient may pass 7 by a little: clamp
-    const int q = max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s))));
-    w |= static_cast<uint32_t>(q + 8) << (4 * i);
+    const float q = x[i] * inv, t = q + kRound;
+    off = fmaxf(off, fabsf(q - (t - kRound)));
+    w |= (__float_as_uint(t) & 15u) << (4 * i);
+  }
+  if (off > 0.499995f || s < 1.17549435e-38f) {
+    w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s))));
+      w |= static_cast<uint32_t>(q + 8) << (4 * i);
+    }
   }
   return w;
 }
 
-// One lane's eight channels of (row `src`, head h) into cache row `row`; whole warps call it (the
-// lanes of a group exchange their amax), `ok` says whether this lane has a row to store.
-template <int DH, typename T>
-__device__ __forceinline__ void append8(const AppendArgs& a, int tensor, int64_t src, int b, int h, int oct, int row,
-                                        bool ok) {
-  constexpr int G = DH / kKv4Group;
-  float x[8] = {};
-  if (ok) load8(static_cast<const T*>(a.x[tensor]) + src * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8, x);
-  uint32_t sb;
-  bool bad;
-  const uint32_t w = quantize8(x, &sb, &bad);
-  if (!ok) return;
-  if (bad) report(a.status, SPATTEN_E_NONFINITE);
-  const int g = oct >> 2, t = oct & 3;
-  const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
-  if (tensor == 0) {
-    reinterpret_cast<uint32_t*>(a.c.k_codes)[at * (DH / 8) + t * G + g] = w;
-  } else {
-    uint16_t* v = reinterpret_cast<uint16_t*>(a.c.v_codes) + at * (DH / 4);
-    v[(2 * t) * G + g] = static_cast<uint16_t>(w);
-    v[(2 * t + 1) * G + g] = static_cast<uint16_t>(w >> 16);
-  }
-  if (t == 0) (tensor == 0 ? a.c.k_scale : a.c.v_scale)[at * G + g] = static_cast<uint16_t>(sb);
+// The lane's octet `oct` of a row as the row's words: K's word as it is; V's runs of four channels of two
+// neighbouring groups make a word, so lanes of groups g and g ^ 1 (four lanes apart) trade halves and
+// keep run 2t (even g) or 2t + 1.
+template <int DH>
+__device__ __forceinline__ uint32_t v_word(uint32_t w, int oct) {
+  const bool odd = (oct >> 2) & 1;
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w & 0xffffu : w >> 16, 4);
+  return odd ? other | (w & 0xffff0000u) : (w & 0xffffu) | other << 16;
+}
+template <int DH>
+__device__ __forceinline__ int k_word_at(int oct) {
+  return (oct & 3) * (DH / 32) + (oct >> 2);
+}
+template <int DH>
+__device__ __forceinline__ int v_word_at(int oct) {
+  const int g = oct >> 2, run = 2 * (oct & 3) + (g & 1);
+  return run * (DH / 64) + (g >> 1);
 }
 
-// Packed rows: one lane per eight channels, blockIdx.y the tensor.  Lanes run along a token's heads,
-// so the loads are whole lines; each row's codes leave as one 32- or 64-byte segment.
+// Stores eight quantized channels of cache row `at` (over all heads and rows); whole warps call it, `ok`
+// says whether this lane has a row.
+template <int DH>
+__device__ __forceinline__ void append8(const AppendArgs& a, int tensor, float* x, int64_t at, int oct, bool ok) {
+  constexpr int G = DH / kKv4Group;
+  uint32_t sb;
+  bool bad;
+  uint32_t w = quantize8(x, &sb, &bad);
+  if (tensor) w = v_word<DH>(w, oct);
+  if (!ok) return;
+  if (bad) report(a.status, SPATTEN_E_NONFINITE);
+  reinterpret_cast<uint32_t*>(tensor ? a.c.v_codes : a.c.k_codes)[at * (DH / 8) + (tensor ? v_word_at<DH>(oct) : k_word_at<DH>(oct))] = w;
+  if ((oct & 3) == 0) (tensor ? a.c.v_scale : a.c.k_scale)[at * G + (oct >> 2)] = static_cast<uint16_t>(sb);
+}
+
+// Packed rows: a warp takes kSteps * 256 / DH rows of one head, eight channels a lane and step, all loads
+// before the first use: rows of a head are whole lines on both sides.  Bound by memory and, next to it, by
+// the quantization's instructions: 16,384 rows of 16 heads of 64 (bfloat16, 86 MB) take <T_APPEND>.
+template <int DH> constexpr int kRowLanes = DH / 8;
+constexpr int kSteps = 4;
+template <int DH> constexpr int kTaskRows = kSteps * 32 / kRowLanes<DH>;
+
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a, bool counts) {
-  constexpr int kLanes = DH / 8;
-  const int per_row = a.c.H_kv * kLanes;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t r = u / per_row;
-  const int rest = static_cast<int>(u - r * per_row), h = rest / kLanes, oct = rest % kLanes;
-  const int tensor = blockIdx.y;
-  bool ok = r < a.total;
-  int b = -1, row = 0, i = 0;
-  if (ok) {
-    b = owner_of_row(a.cu, a.c.B, static_cast<int>(r));
-    ok = b >= 0;
-  }
-  if (ok) {
-    const PackedRows p = packed_rows(a.cu, b, a.total);
-    const int old = clamp_len(a.len[b], a.c.cap, a.status);
-    i = static_cast<int>(r) - p.first;
-    ok = !p.bad && i >= 0 && i < p.n;
-    row = old + i;
-    if (ok && row >= a.c.cap) {
-      report(a.status, SPATTEN_E_INDEX);
-      ok = false;
-    }
-  }
-  append8<DH, T>(a, tensor, r, b, h, oct, row, ok);
-  if (ok && oct == 0 && tensor == 0) {
-    const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
-    if (a.c.weight) a.c.weight[at] = 0.0f;
-    if (a.c.pos) a.c.pos[at] = a.seen[b] + i;
-  }
+  const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>;
   // the counts, where no other block still reads them (len_out and seen_out are buffers of their own)
-  if (counts && blockIdx.y == 0)
-    for (int64_t s = u; s < a.c.B; s += static_cast<int64_t>(gridDim.x) * kThreads) {
+  if (counts)
+    for (int64_t s = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; s < a.c.B; s += static_cast<int64_t>(gridDim.x) * kThreads) {
       const PackedRows p = packed_rows(a.cu, static_cast<int>(s), a.total);
       if (p.bad) report(a.status, SPATTEN_E_INDEX);
       const int old = clamp_len(a.len[s], a.c.cap, a.status), n = min(p.n, a.c.cap - old);
       a.len_out[s] = old + n;
       if (a.seen_out) a.seen_out[s] = a.seen[s] + n;
     }
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int h = static_cast<int>(task % a.c.H_kv);
+  const SeqTile st = find_seq_tile<true>(a.cu, a.c.B, a.total, kTaskRows<DH>, static_cast<int>(task / a.c.H_kv));
+  if (st.b < 0) return;
+  const PackedRows p = packed_rows(a.cu, st.b, a.total);
+  const int old = clamp_len(a.len[st.b], a.c.cap, a.status);
+  const int i0 = st.tile * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);   // rows of the task
+  const int room = a.c.cap - old - i0;                                        // of which these fit
+  if (room < n && lane == 0) report(a.status, SPATTEN_E_INDEX);
+  const int fit = min(n, room);
+  if (fit <= 0) return;
+  const int64_t src = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
+  const int64_t row0 = (static_cast<int64_t>(st.b) * a.c.H_kv + h) * a.c.cap + old + i0;
+  float x[2][kSteps][8];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
+      if (r < fit) {
+        load8(static_cast<const T*>(a.x[t]) + src + r * a.ld_tok, x[t][k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[t][k][i] = 0.0f;
+      }
+    }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
+      append8<DH>(a, t, x[t][k], row0 + r, oct, r < fit);
+    }
+  if (lane < fit) {
+    if (a.c.weight) a.c.weight[row0 + lane] = 0.0f;
+    if (a.c.pos) a.c.pos[row0 + lane] = a.seen[st.b] + i0 + lane;
+  }
 }
 
 // The counts of a call whose outputs are its inputs, after the rows.
@@ -159,11 +196,22 @@ __global__ void __launch_bounds__(kThreads) kv4_append_token_kernel(AppendArgs a
     const int u = u0 + threadIdx.x;
     const int tensor = u >= per_row, rest = u - tensor * per_row, h = rest / kLanes, oct = rest % kLanes;
     const bool ok = room && u < units;
-    append8<DH, T>(a, tensor, b, b, h, oct, row, ok);
-    if (ok && oct == 0 && tensor == 0) {
-      const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
-      if (a.c.weight) a.c.weight[at] = 0.0f;
-      if (a.c.pos) a.c.pos[at] = seen + 0;
+    const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
+    float x[8] = {};
+    if (ok) load8(static_cast<const T*>(a.x[tensor]) + b * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8, x);
+    // per_row is a multiple of 8 lanes: a group's four lanes, and V's pairs of groups, have one tensor
+    uint32_t sb;
+    bool bad;
+    const uint32_t w = quantize8(x, &sb, &bad), v = v_word<DH>(w, oct);
+    if (ok) {
+      if (bad) report(a.status, SPATTEN_E_NONFINITE);
+      uint32_t* codes = reinterpret_cast<uint32_t*>(tensor ? a.c.v_codes : a.c.k_codes) + at * (DH / 8);
+      codes[tensor ? v_word_at<DH>(oct) : k_word_at<DH>(oct)] = tensor ? v : w;
+      if ((oct & 3) == 0) (tensor ? a.c.v_scale : a.c.k_scale)[at * (DH / kKv4Group) + (oct >> 2)] = static_cast<uint16_t>(sb);
+      if (oct == 0 && tensor == 0) {
+        if (a.c.weight) a.c.weight[at] = 0.0f;
+        if (a.c.pos) a.c.pos[at] = seen;
+      }
     }
   }
   __syncthreads();
@@ -180,10 +228,11 @@ int32_t append_launch(const AppendArgs& a, cudaStream_t st) {
     return launch_status();
   }
   const bool apart = a.len_out != a.len && (!a.seen_out || a.seen_out != a.seen);
-  const int64_t units = static_cast<int64_t>(a.total) * a.c.H_kv * (DH / 8);
-  if (units > 0) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(units, kThreads)), 2);
-    kv4_append_kernel<DH, T><<<grid, kThreads, 0, st>>>(a, apart);
+  if (a.total > 0) {
+    // a sequence's rows end in at most one partial task, so this many cover any offsets
+    const int64_t tasks = (static_cast<int64_t>(a.total) / kTaskRows<DH> + a.c.B) * a.c.H_kv, blocks = ceil_div(tasks, kThreads / 32);
+    if (blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
+    kv4_append_kernel<DH, T><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, apart);
     SPT_TRY(launch_status());
     if (apart) return SPATTEN_OK;
   }
@@ -218,45 +267,55 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
   *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// One lane per eight channels; lanes run along a token's heads, so the stores are whole lines.
+// Eight codes in a word's nibbles, times s.
+__device__ __forceinline__ void values8(uint32_t w, float s, float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)   // 2^23 + u, less 2^23 + 8
+    x[i] = s * (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f);
+}
+
+// A warp takes the rows of one head as the append kernel does, all loads before the first use.  Bound by
+// memory: 16,384 rows of 16 heads of 64 to bfloat16 (86 MB) take <T_READ>.
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
-  constexpr int kLanes = DH / 8, G = DH / kKv4Group;
-  const int per_row = a.c.H_kv * kLanes;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t r = u / per_row;
-  if (r >= a.total) return;
-  const int rest = static_cast<int>(u - r * per_row), h = rest / kLanes, oct = rest % kLanes;
-  const int tensor = blockIdx.y;
-  T* out = static_cast<T*>(a.out[tensor]);
-  if (!out) return;
-  const int b = owner_of_row(a.cu, a.c.B, static_cast<int>(r));
-  if (b < 0) return;
-  const PackedRows p = packed_rows(a.cu, b, a.total);
-  const int64_t i = r - p.first;
-  if (p.bad || i < 0 || i >= p.n) {
-    report(a.status, SPATTEN_E_INDEX);
-    return;
-  }
-  const int64_t row = (a.row0 ? a.row0[b] : 0) + i;
-  float x[8] = {};
-  if (row < 0 || row >= a.c.cap) {
-    report(a.status, SPATTEN_E_INDEX);
-  } else {
-    const int g = oct >> 2, t = oct & 3;
-    const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
-    uint32_t w;
-    if (tensor == 0) {
-      w = reinterpret_cast<const uint32_t*>(a.c.k_codes)[at * (DH / 8) + t * G + g];
-    } else {
-      const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v_codes) + at * (DH / 4);
-      w = v[(2 * t) * G + g] | static_cast<uint32_t>(v[(2 * t + 1) * G + g]) << 16;
-    }
-    const float s = bf16_bits_to_float((tensor == 0 ? a.c.k_scale : a.c.v_scale)[at * G + g]);
+  constexpr int G = DH / kKv4Group;
+  const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>, g = oct >> 2;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.c.B; b += kThreads)
+      if (packed_rows(a.cu, b, a.total).bad) report(a.status, SPATTEN_E_INDEX);
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int h = static_cast<int>(task % a.c.H_kv);
+  const SeqTile st = find_seq_tile<true>(a.cu, a.c.B, a.total, kTaskRows<DH>, static_cast<int>(task / a.c.H_kv));
+  if (st.b < 0) return;
+  const PackedRows p = packed_rows(a.cu, st.b, a.total);
+  const int i0 = st.tile * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);
+  const int64_t first = static_cast<int64_t>(a.row0 ? a.row0[st.b] : 0) + i0;   // cache row of the task's first
+  if (lane == 0 && (first < 0 || first + n > a.c.cap)) report(a.status, SPATTEN_E_INDEX);
+  const int64_t base = (static_cast<int64_t>(st.b) * a.c.H_kv + h) * a.c.cap + first;
+  const int64_t dst = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
+  uint32_t w[2][kSteps];
+  float s[2][kSteps];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = s * static_cast<float>(static_cast<int>((w >> (4 * c)) & 15u) - 8);
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
+      const bool ok = r < n && first + r >= 0 && first + r < a.c.cap && a.out[t];   // else 0
+      w[t][k] = ok ? reinterpret_cast<const uint32_t*>(t ? a.c.v_codes : a.c.k_codes)[(base + r) * (DH / 8) + (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct))] : 0u;
+      s[t][k] = ok ? bf16_bits_to_float((t ? a.c.v_scale : a.c.k_scale)[(base + r) * G + g]) : 0.0f;
+    }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    T* out = static_cast<T*>(a.out[t]);
+    if (!out) continue;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
+      float x[8];
+      values8(t ? v_word<DH>(w[t][k], oct) : w[t][k], s[t][k], x);
+      if (r < n) store8(out + dst + r * a.ld_tok, x);
+    }
   }
-  store8(out + r * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8, x);
 }
 
 // ----------------------------------------------------------------------------------------------
@@ -505,8 +564,10 @@ extern "C" int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* c
   if (!aligned16(k_out) || !aligned16(v_out) || (ld_tok * esz) % 16 != 0) return SPATTEN_E_ALIGN;
   if (total == 0) return SPATTEN_OK;
   const ReadArgs a{*c, cu, row0, total, {k_out, v_out}, ld_tok, dev_status};
-  const int64_t units = static_cast<int64_t>(total) * c->H_kv * (c->d_h / 8);
-  const dim3 grid(static_cast<unsigned>(ceil_div(units, kThreads)), 2);
+  const int64_t tasks = (static_cast<int64_t>(total) / (c->d_h == 64 ? kTaskRows<64> : kTaskRows<128>) + c->B) * c->H_kv;
+  const int64_t blocks = ceil_div(tasks, kThreads / 32);
+  if (blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(blocks);
   cudaStream_t st = as_stream(stream);
   if (c->d_h == 64) {
     if (dtype == SPATTEN_BF16) kv4_read_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, st>>>(a);

@@ -39,6 +39,43 @@ __device__ __forceinline__ int owner_of_row(const int32_t* cu, int B, int r) {
   return lo;
 }
 
+// The sequence and tile number t, for tiles of `rows` packed rows that start anew at each sequence:
+// tiles are counted from the last sequence's last tile backwards, so that a sequence's late rows, which
+// see the most keys, are started first (FRONT: from the first sequence's first tile).  Every warp calls
+// it whole; b = -1 past the last tile.
+struct SeqTile {
+  int b, tile;
+};
+template <bool FRONT = false>
+__device__ __forceinline__ SeqTile find_seq_tile(const int32_t* cu, int B, int total, int rows, int t) {
+  const int lane = threadIdx.x & 31;
+  int all = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int c = b0 + lane < B ? (packed_rows(cu, b0 + lane, total).n + rows - 1) / rows : 0;
+    all += warp_sum_int(c);
+  }
+  int want = FRONT ? t : all - 1 - t;
+  if (want < 0 || want >= all) return {-1, 0};
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int c = b0 + lane < B ? (packed_rows(cu, b0 + lane, total).n + rows - 1) / rows : 0;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int sum = __shfl_sync(0xffffffffu, inc, 31);
+    if (want < sum) {
+      const uint32_t past = __ballot_sync(0xffffffffu, want < inc);
+      const int l = __ffs(past) - 1;
+      const int before = __shfl_sync(0xffffffffu, inc - c, l);
+      return {b0 + l, want - before};
+    }
+    want -= sum;
+  }
+  return {-1, 0};
+}
+
 // A row count from the device, held to [0, most]; a count outside is reported.
 __device__ __forceinline__ int clamp_len(int n, int most, int32_t* status) {
   if (n < 0 || n > most) {
