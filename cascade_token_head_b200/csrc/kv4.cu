@@ -34,48 +34,116 @@ struct AppendArgs {
   int32_t* status;
 };
 
-// Eight channels (one lane's share: a quarter of a 32-channel group) of one row to codes; the four
-// lanes of the group share their amax; whole warps call it.  Returns the codes as nibbles (channel i at
-// bits 4i) and the scale's bfloat16 bits.
-// The code is rint(x / s) of the IEEE quotient.  The product with an approximate reciprocal is off by less
-// than 2e-6 here, so its rounding is the quotient's unless it lies that near to a half; such lanes, and
-// subnormal scales (where the quotient may pass 7), divide.
-__device__ __forceinline__ uint32_t quantize8(float* x, uint32_t* scale_bits, bool* bad) {
-  float z = 0.0f, amax = 0.0f;
+// Eight channels as they are loaded.
+struct Bf16x8 {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float* x) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z = fmaf(x[i], 0.0f, z);   // NaN if any is not finite
-  *bad = z != 0.0f;
-  if (*bad)
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  // bits of the largest magnitude; a NaN counts as larger than infinity
+  __device__ __forceinline__ uint32_t absmax() const {
+    constexpr uint32_t M = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & M, u.y & M), __vmaxu2(u.z & M, u.w & M));
+    return max(m << 16, m & 0xffff0000u);
+  }
+};
+struct F32x8 {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ uint32_t absmax() const {
+    float x[8];
+    get(x);
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = isfinite(x[i]) ? x[i] : 0.0f;
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+  }
+};
+template <typename T> struct Octet { using type = Bf16x8; };
+template <> struct Octet<float> { using type = F32x8; };
+
+// What quantize8 does, by IEEE divisions: the codes, and the scale's bits with bit 31 set where this lane
+// held a value that is not finite.
+__device__ __noinline__ uint2 quantize8_by_division(float4 a, float4 b) {
+  float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  bool bad = false;
+  float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) {
+    if (!isfinite(x[i])) {
+      x[i] = 0.0f;
+      bad = true;
+    }
+    amax = fmaxf(amax, fabsf(x[i]));
+  }
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
   if (__bfloat162float(sb) == 0.0f) sb = __float2bfloat16_rn(1.0f);
   const float s = __bfloat162float(sb);
-  *scale_bits = __bfloat16_as_ushort(sb);
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  constexpr float kRound = 12582912.0f + 8.0f;   // 1.5 * 2^23 + 8: the sum's low bits are rint(x / s) + 8
   uint32_t w = 0;
-  float off = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = x[i] * inv, t = q + kRound;
-    off = fmaxf(off, fabsf(q - (t - kRound)));
-    w |= (__float_as_uint(t) & 15u) << (4 * i);
+    const int q = max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s))));
+    w |= static_cast<uint32_t>(q + 8) << (4 * i);
   }
-  if (off > 0.499995f || s < 1.17549435e-38f) {
-    w = 0;
+  return make_uint2(w, static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (bad ? 0x80000000u : 0u));
+}
+
+// Eight channels (one lane's share: a quarter of a 32-channel group) of one row to codes; the four
+// lanes of the group share their amax; whole warps call it.  Returns the codes as nibbles (channel i at
+// bits 4i) and the scale's bfloat16 bits.
+// Both roundings are those of IEEE quotients.  amax (1 / 7) is within 2 steps of the quotient, so both
+// round to the same bfloat16 unless it is that near to a border.  x / s is rounded as the quotient is by
+// Markstein's theorem (1990): with y = 1 / s rounded to nearest, q = x y and r = x - q s, which is exact,
+// q + r y rounds to the nearest x / s (s is no number of all ones: it has eight bits).  Borders, values
+// that are not finite and scales below 2^-100, where products underflow and the quotient may pass 7, make
+// the warp divide; elsewhere the quotient is at most 7 (1 + 2^-8).  Dividing everywhere took 1.7 times as
+// long (16,384 rows of 16 heads of 64).
+template <typename X>
+__device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits, bool* bad) {
+  float x[8];
+  raw.get(x);
+  uint32_t am = raw.absmax();
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  const uint32_t q7 = __float_as_uint(__uint_as_float(am) * (1.0f / 7.0f));
+  uint32_t sb = (q7 + 0x7fffu + ((q7 >> 16) & 1u)) >> 16;   // to the nearest bfloat16
+  *bad = false;
+  const bool zero = am == 0;
+  if (__any_sync(0xffffffffu, am >= 0x7f800000u || (q7 & 0xffffu) - 0x7ffcu <= 8u || (sb < (27u << 7) && !zero))) {
+    const uint2 r = quantize8_by_division(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]));
+    *scale_bits = r.y & 0xffffu;
+    *bad = r.y >> 31;
+    return r.x;
+  }
+  sb = zero ? 0x3f80u : sb;
+  *scale_bits = sb;
+  const float s = __uint_as_float(sb << 16), y = __frcp_rn(s);
+  const float2 y2 = make_float2(y, y), s2 = make_float2(-s, -s);
+  constexpr float kCodeRound = 12582912.0f + 8.0f;   // 1.5 * 2^23 + 8: the sum's low bits are rint(x / s) + 8
+  const float2 up = make_float2(kCodeRound, kCodeRound);
+  uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s))));
-      w |= static_cast<uint32_t>(q + 8) << (4 * i);
-    }
+  for (int i = 0; i < 8; i += 2) {
+    const float2 v = make_float2(x[i], x[i + 1]), q = __fmul2_rn(v, y2);
+    const float2 t = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, s2, v), y2, q), up);
+    // the sums' high bits are constants, which drop out at the end
+    w += __float_as_uint(t.x) * (1u << (4 * i)) + __float_as_uint(t.y) * (16u << (4 * i));
   }
-  return w;
+  constexpr uint32_t kHigh = 0x4b400000u * 0x11111111u;
+  return w - kHigh;
 }
 
 // The lane's octet `oct` of a row as the row's words: K's word as it is; V's runs of four channels of two
@@ -99,8 +167,8 @@ __device__ __forceinline__ int v_word_at(int oct) {
 
 // Stores eight quantized channels of cache row `at` (over all heads and rows); whole warps call it, `ok`
 // says whether this lane has a row.
-template <int DH>
-__device__ __forceinline__ void append8(const AppendArgs& a, int tensor, float* x, int64_t at, int oct, bool ok) {
+template <int DH, typename X>
+__device__ __forceinline__ void append8(const AppendArgs& a, int tensor, const X& x, int64_t at, int oct, bool ok) {
   constexpr int G = DH / kKv4Group;
   uint32_t sb;
   bool bad;
@@ -118,12 +186,29 @@ __device__ __forceinline__ void append8(const AppendArgs& a, int tensor, float* 
 template <int DH> constexpr int kRowLanes = DH / 8;
 constexpr int kSteps = 4;
 template <int DH> constexpr int kTaskRows = kSteps * 32 / kRowLanes<DH>;
+template <int DH> constexpr int kBlockRows = kTaskRows<DH> * (kThreads / 32);   // of one sequence
+
+// The rows i0 .. of sequence b (n rows from packed row `first`) that block blockIdx.x works on; b = -1: none.
+// The whole block calls it, once.
+struct BlockRows {
+  int b, i0, first, n;
+};
+__device__ __forceinline__ BlockRows find_block_rows(const int32_t* cu, int B, int total, int rows) {
+  __shared__ BlockRows sh;
+  if (threadIdx.x < 32) {
+    const SeqTile st = find_seq_tile<true>(cu, B, total, rows, blockIdx.x);
+    const PackedRows p = st.b < 0 ? PackedRows{0, 0, false} : packed_rows(cu, st.b, total);
+    if (threadIdx.x == 0) sh = {st.b, st.tile * rows, p.first, p.n};
+  }
+  __syncthreads();
+  return sh;
+}
 
 template <int DH, typename T>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a, bool counts) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, bool counts) {
   const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>;
   // the counts, where no other block still reads them (len_out and seen_out are buffers of their own)
-  if (counts)
+  if (counts && blockIdx.y == 0)
     for (int64_t s = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; s < a.c.B; s += static_cast<int64_t>(gridDim.x) * kThreads) {
       const PackedRows p = packed_rows(a.cu, static_cast<int>(s), a.total);
       if (p.bad) report(a.status, SPATTEN_E_INDEX);
@@ -131,42 +216,35 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a, bool
       a.len_out[s] = old + n;
       if (a.seen_out) a.seen_out[s] = a.seen[s] + n;
     }
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int h = static_cast<int>(task % a.c.H_kv);
-  const SeqTile st = find_seq_tile<true>(a.cu, a.c.B, a.total, kTaskRows<DH>, static_cast<int>(task / a.c.H_kv));
-  if (st.b < 0) return;
-  const PackedRows p = packed_rows(a.cu, st.b, a.total);
-  const int old = clamp_len(a.len[st.b], a.c.cap, a.status);
-  const int i0 = st.tile * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);   // rows of the task
-  const int room = a.c.cap - old - i0;                                        // of which these fit
+  const int h = blockIdx.y;
+  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH>);
+  const int i0 = p.i0 + (threadIdx.x >> 5) * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);   // rows of the warp
+  if (p.b < 0 || n <= 0) return;
+  const int old = clamp_len(a.len[p.b], a.c.cap, a.status);
+  const int room = a.c.cap - old - i0;   // of which these fit
   if (room < n && lane == 0) report(a.status, SPATTEN_E_INDEX);
   const int fit = min(n, room);
   if (fit <= 0) return;
   const int64_t src = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
-  const int64_t row0 = (static_cast<int64_t>(st.b) * a.c.H_kv + h) * a.c.cap + old + i0;
-  float x[2][kSteps][8];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      if (r < fit) {
-        load8(static_cast<const T*>(a.x[t]) + src + r * a.ld_tok, x[t][k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[t][k][i] = 0.0f;
-      }
-    }
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
+  const int64_t row0 = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap + old + i0;
+#pragma unroll 1   // unrolled it is too large for the instruction cache
+  for (int t = 0; t < 2; ++t) {
+    typename Octet<T>::type x[kSteps];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      append8<DH>(a, t, x[t][k], row0 + r, oct, r < fit);
+      if (r < fit) x[k].load(static_cast<const T*>(t ? a.x[1] : a.x[0]) + src + r * a.ld_tok);
+      else x[k].zero();
     }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
+      append8<DH>(a, t, x[k], row0 + r, oct, r < fit);
+    }
+  }
   if (lane < fit) {
     if (a.c.weight) a.c.weight[row0 + lane] = 0.0f;
-    if (a.c.pos) a.c.pos[row0 + lane] = a.seen[st.b] + i0 + lane;
+    if (a.c.pos) a.c.pos[row0 + lane] = a.seen[p.b] + i0 + lane;
   }
 }
 
@@ -197,8 +275,9 @@ __global__ void __launch_bounds__(kThreads) kv4_append_token_kernel(AppendArgs a
     const int tensor = u >= per_row, rest = u - tensor * per_row, h = rest / kLanes, oct = rest % kLanes;
     const bool ok = room && u < units;
     const int64_t at = (static_cast<int64_t>(b) * a.c.H_kv + h) * a.c.cap + row;
-    float x[8] = {};
-    if (ok) load8(static_cast<const T*>(a.x[tensor]) + b * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8, x);
+    typename Octet<T>::type x;
+    if (ok) x.load(static_cast<const T*>(a.x[tensor]) + b * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8);
+    else x.zero();
     // per_row is a multiple of 8 lanes: a group's four lanes, and V's pairs of groups, have one tensor
     uint32_t sb;
     bool bad;
@@ -229,10 +308,9 @@ int32_t append_launch(const AppendArgs& a, cudaStream_t st) {
   }
   const bool apart = a.len_out != a.len && (!a.seen_out || a.seen_out != a.seen);
   if (a.total > 0) {
-    // a sequence's rows end in at most one partial task, so this many cover any offsets
-    const int64_t tasks = (static_cast<int64_t>(a.total) / kTaskRows<DH> + a.c.B) * a.c.H_kv, blocks = ceil_div(tasks, kThreads / 32);
-    if (blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
-    kv4_append_kernel<DH, T><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, apart);
+    // a sequence's rows end in at most one partial run, so this many cover any offsets
+    const dim3 grid(a.total / kBlockRows<DH> + a.c.B, a.c.H_kv);
+    kv4_append_kernel<DH, T><<<grid, kThreads, 0, st>>>(a, apart);
     SPT_TRY(launch_status());
     if (apart) return SPATTEN_OK;
   }
@@ -253,25 +331,27 @@ struct ReadArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    r[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-// Eight codes in a word's nibbles, times s.
-__device__ __forceinline__ void values8(uint32_t w, float s, float* x) {
+// Stores the eight codes of a word times a scale (bfloat16 bits).
+__device__ __forceinline__ void store_values(float* p, uint32_t w, uint32_t sb) {
+  const float s = bf16_bits_to_float(sb);
+  float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)   // 2^23 + u, less 2^23 + 8
     x[i] = s * (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f);
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+// In bfloat16 the code is exact and the product is rounded once, as the float32 product would be.
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint32_t sb) {
+  const uint32_t s2 = sb | sb << 16;
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // channels i, i + 4: 128 + u, less 136
+    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("{\n.reg .b32 t;\nadd.rn.bf16x2 t, %1, %2;\nmul.rn.bf16x2 %0, t, %3;\n}" : "=r"(v[i]) : "r"(u), "r"(0xc308c308u), "r"(s2));
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                                            __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
 // A warp takes the rows of one head as the append kernel does, all loads before the first use.  Bound by
@@ -280,21 +360,19 @@ template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
   constexpr int G = DH / kKv4Group;
   const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>, g = oct >> 2;
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = threadIdx.x; b < a.c.B; b += kThreads)
       if (packed_rows(a.cu, b, a.total).bad) report(a.status, SPATTEN_E_INDEX);
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int h = static_cast<int>(task % a.c.H_kv);
-  const SeqTile st = find_seq_tile<true>(a.cu, a.c.B, a.total, kTaskRows<DH>, static_cast<int>(task / a.c.H_kv));
-  if (st.b < 0) return;
-  const PackedRows p = packed_rows(a.cu, st.b, a.total);
-  const int i0 = st.tile * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);
-  const int64_t first = static_cast<int64_t>(a.row0 ? a.row0[st.b] : 0) + i0;   // cache row of the task's first
+  const int h = blockIdx.y;
+  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH>);
+  const int i0 = p.i0 + (threadIdx.x >> 5) * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);
+  if (p.b < 0 || n <= 0) return;
+  const int64_t first = static_cast<int64_t>(a.row0 ? a.row0[p.b] : 0) + i0;   // cache row of the task's first
   if (lane == 0 && (first < 0 || first + n > a.c.cap)) report(a.status, SPATTEN_E_INDEX);
-  const int64_t base = (static_cast<int64_t>(st.b) * a.c.H_kv + h) * a.c.cap + first;
+  const int64_t base = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap + first;
   const int64_t dst = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
   uint32_t w[2][kSteps];
-  float s[2][kSteps];
+  uint32_t s[2][kSteps];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -302,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
       const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
       const bool ok = r < n && first + r >= 0 && first + r < a.c.cap && a.out[t];   // else 0
       w[t][k] = ok ? reinterpret_cast<const uint32_t*>(t ? a.c.v_codes : a.c.k_codes)[(base + r) * (DH / 8) + (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct))] : 0u;
-      s[t][k] = ok ? bf16_bits_to_float((t ? a.c.v_scale : a.c.k_scale)[(base + r) * G + g]) : 0.0f;
+      s[t][k] = ok ? (t ? a.c.v_scale : a.c.k_scale)[(base + r) * G + g] : 0u;
     }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -311,9 +389,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      float x[8];
-      values8(t ? v_word<DH>(w[t][k], oct) : w[t][k], s[t][k], x);
-      if (r < n) store8(out + dst + r * a.ld_tok, x);
+      const uint32_t u = t ? v_word<DH>(w[t][k], oct) : w[t][k];
+      if (r < n) store_values(out + dst + r * a.ld_tok, u, s[t][k]);
     }
   }
 }
@@ -564,10 +641,7 @@ extern "C" int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* c
   if (!aligned16(k_out) || !aligned16(v_out) || (ld_tok * esz) % 16 != 0) return SPATTEN_E_ALIGN;
   if (total == 0) return SPATTEN_OK;
   const ReadArgs a{*c, cu, row0, total, {k_out, v_out}, ld_tok, dev_status};
-  const int64_t tasks = (static_cast<int64_t>(total) / (c->d_h == 64 ? kTaskRows<64> : kTaskRows<128>) + c->B) * c->H_kv;
-  const int64_t blocks = ceil_div(tasks, kThreads / 32);
-  if (blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const dim3 grid(total / (c->d_h == 64 ? kBlockRows<64> : kBlockRows<128>) + c->B, c->H_kv);
   cudaStream_t st = as_stream(stream);
   if (c->d_h == 64) {
     if (dtype == SPATTEN_BF16) kv4_read_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
