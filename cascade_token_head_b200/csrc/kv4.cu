@@ -1,6 +1,10 @@
 // The 4-bit cache: append (quantize new rows), read (rows back as values) and evict (give up the
 // rows with the least attention weight).  Layout and rules: spatten.h.
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace spt {
 
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
 // ----------------------------------------------------------------------------------------------
 // evict
 // ----------------------------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024;   // of the two-launch form
 
 struct EvictArgs {
   spatten_kv4_cache s, d;
@@ -417,160 +421,401 @@ struct EvictArgs {
   int32_t* status;
 };
 
+// A row's rank as a number, larger first: rows with pos >= safe_from before all others, NaN weights last.
+__device__ __forceinline__ uint32_t key_of(float w, int pos, int safe_from, bool has_safe) {
+  return has_safe && pos >= safe_from ? 0xffffffffu : (isnan(w) ? 0u : float_key(w));
+}
 __device__ __forceinline__ uint32_t row_key(const EvictArgs& a, int64_t base, int j, int safe_from, bool has_safe) {
-  if (has_safe && a.s.pos[base + j] >= safe_from) return 0xffffffffu;
-  const float w = a.s.weight[base + j];
-  return isnan(w) ? 0u : float_key(w);
+  return key_of(a.s.weight[base + j], has_safe ? a.s.pos[base + j] : 0, safe_from, has_safe);
 }
 
-// Exclusive prefix sums of two flags over the block in thread order; totals in *t0, *t1.
-__device__ __forceinline__ int2 block_rank(bool f0, bool f1, int2* warp_sums, int* t0, int* t1) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t m0 = __ballot_sync(0xffffffffu, f0), m1 = __ballot_sync(0xffffffffu, f1);
-  if (lane == 0) warp_sums[warp] = make_int2(__popc(m0), __popc(m1));
-  __syncthreads();
-  int2 w = warp_sums[lane];   // 32 warps: every warp scans all sums
-  int2 inc = w;
+// Inclusive prefix sum over a warp.
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
-    if (lane >= o) {
-      inc.x += x;
-      inc.y += y;
-    }
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
   }
-  *t0 = __shfl_sync(0xffffffffu, inc.x, 31);
-  *t1 = __shfl_sync(0xffffffffu, inc.y, 31);
-  const int bx = __shfl_sync(0xffffffffu, inc.x - w.x, warp), by = __shfl_sync(0xffffffffu, inc.y - w.y, warp);
+  return v;
+}
+// Sum of the counts of the warps before this one; *all: of all of them.  Every lane of a warp gives the
+// warp's count.  One barrier; `sums` is not used again before the next one.
+template <int THREADS>
+__device__ __forceinline__ int before_warp(int count, int* sums, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) sums[warp] = count;
   __syncthreads();
-  const uint32_t below = (1u << lane) - 1u;
-  return make_int2(bx + __popc(m0 & below), by + __popc(m1 & below));
+  const int c = lane < THREADS / 32 ? sums[lane] : 0, inc = warp_scan(c);
+  *all = __shfl_sync(0xffffffffu, inc, 31);
+  return __shfl_sync(0xffffffffu, inc - c, warp);
 }
 
-// One block per (sequence, head): the keep-th largest key by four 8-bit radix passes, then one pass
-// in row order that ranks ties, holes and the rows that fill them.
+struct Threshold {
+  uint32_t key;   // the k-th largest key
+  int ties;       // how many rows with this key stay,
+  bool all;       // which are all of them
+};
+
+constexpr int kBins = 2048;   // digits of 11, 11 and 10 bits
+
+// The k-th largest of n keys (1 <= k <= n) by three radix passes; get(j) gives the keys of rows j .. j + 3 (j a
+// multiple of 4; any number past n); `hist` has kBins entries.
+template <int THREADS, typename Get>
+__device__ __forceinline__ Threshold radix_select(int n, int k, Get get, int* hist, int (*sums)[32]) {
+  __shared__ Threshold found;
+  const int tid = threadIdx.x;
+  uint32_t prefix = 0;
+  int want = k;
+  bool all_stay = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? kBins / 2 : kBins;
+    // thread t has the t-th `per` bins; bin b's count lies where the threads' i-th ones are neighbours
+    const int per = bins / THREADS, log_per = 31 - __clz(per);
+    auto place = [&](int b) { return (b & (per - 1)) * THREADS + (b >> log_per); };
+    for (int i = tid; i < bins; i += THREADS) hist[i] = 0;
+    __syncthreads();
+    const uint32_t above = pass == 0 ? 0u : (pass == 1 ? ~0u << 21 : ~0u << 10);
+#pragma unroll 2
+    for (int j0 = 0; j0 < n; j0 += 4 * THREADS) {
+      const int j = j0 + 4 * tid;
+      const uint4 q = j < n ? get(j) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+      int bin[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        bin[u] = j + u < n && (key[u] & above) == prefix ? static_cast<int>((key[u] >> shift) & (bins - 1u)) : -1;
+      // equal weights (a new cache's zeros) would queue up at one bin: a warp of one bin adds once
+      int one;
+      __match_all_sync(0xffffffffu, bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3] ? bin[0] : -2 - (tid & 31), &one);
+      if (one) {
+        if (bin[0] >= 0 && (tid & 31) == 0) atomicAdd(&hist[place(bin[0])], 128);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (bin[u] >= 0) atomicAdd(&hist[place(bin[u])], 1);
+      }
+    }
+    __syncthreads();
+    // from the largest: thread t adds up those of thread THREADS - 1 - t
+    int c[kBins / THREADS], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / THREADS; ++i) {
+      c[i] = i < per ? hist[place(bins - 1 - tid * per - i)] : 0;
+      sum += c[i];
+    }
+    const int inc = warp_scan(sum);
+    int all;
+    int before = before_warp<THREADS>(__shfl_sync(0xffffffffu, inc, 31), sums[pass & 1], &all) + inc - sum;
+    if (before < want && want <= before + sum) {
+#pragma unroll
+      for (int i = 0; i < kBins / THREADS; ++i) {
+        if (before < want && want <= before + c[i])
+          found = {prefix | static_cast<uint32_t>(bins - 1 - tid * per - i) << shift, want - before, want == before + c[i]};
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    prefix = found.key;
+    want = found.ties;
+    all_stay = found.all;
+  }
+  return {prefix, want, all_stay};
+}
+
+// Of flags in row order (four rows a lane, bit u of `bits` the u-th): how many are set in the lanes before
+// this one; *total: in the warp.
+__device__ __forceinline__ int flags_before(uint32_t bits, int* total) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+  int before = 0;
+  *total = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t m = __ballot_sync(0xffffffffu, (bits >> u) & 1u);
+    before += __popc(m & below);
+    *total += __popc(m);
+  }
+  return before;
+}
+
+// Ranks the rows in their order, each warp a run of them, each lane rows j .. j + 3: low(j, holes, i) names the
+// rows below k among them that go (bits of `holes`), the first of which is the i-th such row of all;
+// high(j, tails, i) so the rows from k on that stay.  Returns the number of either.
+template <int THREADS, typename Get, typename Low, typename High>
+__device__ __forceinline__ int rank_rows(int n, int k, Threshold th, Get get, int (*sums)[32], Low low_rows, High high_rows) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int run = (n + 4 * THREADS - 1) / (4 * THREADS) * 128, j0 = min(n, warp * run), j1 = min(n, j0 + run);
+  // rows j .. j + 3 of a lane: which have the threshold's key, and which a larger one
+  auto compare = [&](int j, uint32_t& ties) {
+    const uint4 q = j < j1 ? get(j) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+    uint32_t larger = 0;
+    ties = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      larger |= (j + u < j1 && key[u] > th.key ? 1u : 0u) << u;
+      ties |= (j + u < j1 && key[u] == th.key ? 1u : 0u) << u;
+    }
+    return larger;
+  };
+  int t0 = 0, all;
+  if (!th.all) {   // of the ties the first ones stay: they are ranked first
+    int ties = 0;
+    for (int jw = j0; jw < j1; jw += 128) {
+      uint32_t bits;
+      compare(jw + 4 * lane, bits);
+      ties += __popc(bits);
+    }
+    t0 = before_warp<THREADS>(warp_sum_int(ties), sums[0], &all);
+  }
+  auto kept_rows = [&](int j, int& t) {
+    uint32_t ties;
+    const uint32_t larger = compare(j, ties);
+    if (th.all) return larger | ties;
+    int total, r = t + flags_before(ties, &total);
+    t += total;
+    uint32_t kept = larger;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if ((ties >> u) & 1u) kept |= (r++ < th.ties ? 1u : 0u) << u;
+    return kept;
+  };
+  // masks of the rows below k, and of the rows there are
+  auto rows_to = [&](int j, int end) { return (1u << max(0, min(4, end - j))) - 1u; };
+  int holes = 0, tails = 0, t = t0;
+  for (int jw = j0; jw < j1; jw += 128) {
+    const int j = jw + 4 * lane;
+    const uint32_t kept = kept_rows(j, t), low = rows_to(j, min(k, j1));
+    holes += __popc(low & ~kept);
+    tails += __popc(kept & ~rows_to(j, k));
+  }
+  int moved;
+  int h = before_warp<THREADS>(warp_sum_int(holes), sums[1], &moved), w = before_warp<THREADS>(warp_sum_int(tails), sums[2], &all);
+  t = t0;
+  for (int jw = j0; jw < j1; jw += 128) {
+    const int j = jw + 4 * lane;
+    const uint32_t kept = kept_rows(j, t), low = rows_to(j, min(k, j1));
+    const uint32_t is_hole = low & ~kept, is_tail = kept & ~rows_to(j, k);
+    int n_hole, n_tail;
+    if (jw < k) {
+      low_rows(j, is_hole, h + flags_before(is_hole, &n_hole));
+      h += n_hole;
+    }
+    if (jw + 128 > k) {
+      high_rows(j, is_tail, w + flags_before(is_tail, &n_tail));
+      w += n_tail;
+    }
+  }
+  return moved;
+}
+
+// Moves rows i < n of a (sequence, head): rows(i, &to, &from) names them; thread `me` of `threads`.  First
+// the codes, 16-byte pieces of K and V side by side, then words: the scales, the weight, the position.  Lanes
+// of one kind of piece in separate branches would wait for memory once a kind; so they differ by pointers.
+template <int DH, typename Rows>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int64_t s_base, int64_t d_base, int n, int me, int threads, Rows rows) {
+  {
+    constexpr int kCode = DH / 32, kLanes = 2 * kCode, kU = 4;
+    const int piece = me % kLanes, step = threads / kLanes;
+    const bool v = piece >= kCode;
+    const uint4* src = reinterpret_cast<const uint4*>(v ? a.s.v_codes : a.s.k_codes) + s_base * kCode + piece % kCode;
+    uint4* dst = reinterpret_cast<uint4*>(v ? a.d.v_codes : a.d.k_codes) + d_base * kCode + piece % kCode;
+    for (int i0 = me / kLanes; i0 < n; i0 += kU * step) {
+      uint4 x[kU];
+      int to[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        int from;
+        to[u] = -1;
+        if (i0 + u * step < n) {
+          rows(i0 + u * step, to[u], from);
+          x[u] = src[static_cast<int64_t>(from) * kCode];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (to[u] >= 0) dst[static_cast<int64_t>(to[u]) * kCode] = x[u];
+    }
+  }
+  {
+    constexpr int kScale = DH / 64, kLanes = DH == 64 ? 4 : 8, kU = 8;   // words of a row's scales; 128 channels: 6 in use
+    const int piece = me % kLanes, step = threads / kLanes;
+    const bool v = piece >= kScale, scale = piece < 2 * kScale, weight = piece == 2 * kScale;
+    const int width = scale ? kScale : 1, at = scale ? piece % kScale : 0;
+    const uint32_t* src = scale ? reinterpret_cast<const uint32_t*>(v ? a.s.v_scale : a.s.k_scale)
+                                : (weight ? reinterpret_cast<const uint32_t*>(a.s.weight) : reinterpret_cast<const uint32_t*>(a.s.pos));
+    uint32_t* dst = scale ? reinterpret_cast<uint32_t*>(v ? a.d.v_scale : a.d.k_scale)
+                          : (weight ? reinterpret_cast<uint32_t*>(a.d.weight) : reinterpret_cast<uint32_t*>(a.d.pos));
+    if (piece > 2 * kScale + 1 || !src) n = 0;
+    src += s_base * width + at;
+    dst += d_base * width + at;
+    for (int i0 = me / kLanes; i0 < n; i0 += kU * step) {
+      uint32_t x[kU];
+      int to[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        int from;
+        to[u] = -1;
+        if (i0 + u * step < n) {
+          rows(i0 + u * step, to[u], from);
+          x[u] = src[static_cast<int64_t>(from) * width];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (to[u] >= 0) dst[static_cast<int64_t>(to[u]) * width] = x[u];
+    }
+  }
+}
+
+__device__ __forceinline__ void report_nan(const EvictArgs& a, int64_t base, int n) {
+  bool bad = false;
+  for (int j = threadIdx.x; j < n; j += kSelThreads) bad |= isnan(a.s.weight[base + j]);
+  if (bad) report(a.status, SPATTEN_E_NONFINITE);
+}
+
+// One launch: a cluster per (sequence, head).  Each of its CTAs selects on its own, from keys in shared memory
+// (so that nothing but the end of the selection has to be agreed on), and then moves its share of the rows.
+// The work per row is small: what is bounded is latency (radix passes and ranks: 5 us for 1152 rows).
+template <int DH, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_evict_kernel(EvictArgs a) {
+  extern __shared__ __align__(16) uint32_t keys[];   // [n_max] keys (to a multiple of 4), then the lists
+  __shared__ int hist[kBins], sums[3][32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = gridDim.x, rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, k = a.keep;
+  const int64_t bh = static_cast<int64_t>(b) * a.s.H_kv + h, base = bh * a.s.cap, d_base = bh * a.d.cap;
+  const int n = clamp_len(a.len[b], a.n_max, a.status);
+  if (a.len_out != a.len && rank == 0 && h == 0 && tid == 0) a.len_out[b] = min(n, k);
+  int* tail = reinterpret_cast<int*>(keys) + (a.n_max + 3) / 4 * 4;   // [m]
+  int* list = tail + (a.m + 3) / 4 * 4;   // in place [m]: the holes; else [keep]: row, or -1 - i for the i-th hole
+  int moves = a.in_place ? 0 : n;
+  const bool select = n > k;
+  if (select) {
+    const bool has_safe = a.recent > 0;
+    const int safe_from = has_safe ? a.seen[b] - a.recent : 0;
+    bool bad = false;
+    for (int j0 = tid; j0 < n; j0 += 8 * THREADS) {
+      float w[8];
+      int pos[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {   // all loads before the first use
+        const int j = j0 + u * THREADS;
+        w[u] = j < n ? a.s.weight[base + j] : 0.0f;
+        pos[u] = j < n && has_safe ? a.s.pos[base + j] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = j0 + u * THREADS;
+        bad |= isnan(w[u]);
+        if (j < n) keys[j] = key_of(w[u], pos[u], safe_from, has_safe);
+      }
+    }
+    if (bad && rank == 0) report(a.status, SPATTEN_E_NONFINITE);
+    auto get = [&](int j) { return *reinterpret_cast<const uint4*>(keys + j); };
+    const Threshold th = radix_select<THREADS>(n, k, get, hist, sums);   // its first barrier: the keys are there
+    const bool in_place = a.in_place;
+    moves = rank_rows<THREADS>(
+        n, k, th, get, sums,
+        [&](int j, uint32_t holes, int i) {
+          if (in_place) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if ((holes >> u) & 1u) list[i++] = j + u;
+          } else if (j < k) {   // whole words: the list is padded to a multiple of four
+            int x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool hole = (holes >> u) & 1u;
+              x[u] = hole ? -1 - i : j + u;
+              i += hole;
+            }
+            *reinterpret_cast<int4*>(list + j) = make_int4(x[0], x[1], x[2], x[3]);
+          }
+        },
+        [&](int j, uint32_t tails, int i) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if ((tails >> u) & 1u) tail[i++] = j + u;
+        });
+    if (!in_place) moves = k;
+  }
+  if (C > 1 && a.in_place) cluster.sync();   // every CTA has read the weights and positions
+  else __syncthreads();
+  move_rows<DH>(a, base, d_base, moves, rank * THREADS + tid, C * THREADS,
+                [&](int i, int& to, int& from) {
+                  if (a.in_place) {
+                    to = list[i];
+                    from = tail[i];
+                  } else {
+                    const int f = select ? list[i] : i;
+                    to = i;
+                    from = f < 0 ? tail[-1 - f] : f;
+                  }
+                });
+}
+
+__global__ void __launch_bounds__(kThreads) kv4_evict_counts_kernel(EvictArgs a) {
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.s.B; b += gridDim.x * kThreads)
+    a.len_out[b] = min(clamp_len(a.len[b], a.n_max, nullptr), a.keep);
+}
+
+// Caches whose keys and lists do not fit shared memory: one CTA per (sequence, head) selects from the weights
+// themselves and writes the moves to the workspace, a second launch moves.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int2 warp_sums[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_want;
+  __shared__ int hist[kBins], sums[3][32];
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int64_t bh = static_cast<int64_t>(b) * a.s.H_kv + h, base = bh * a.s.cap;
   const int n = clamp_len(a.len[b], a.n_max, a.status), k = a.keep;
-  if (n <= k) {
-    if (tid == 0) {
-      a.count[2 * bh] = a.in_place ? 0 : n;
-      a.count[2 * bh + 1] = n;
-    }
-    if (!a.in_place)
-      for (int i = tid; i < n; i += kSelThreads) a.from[bh * a.keep + i] = i;
-    return;
-  }
-  const bool has_safe = a.recent > 0;
-  const int safe_from = has_safe ? a.seen[b] - a.recent : 0;
-  uint32_t prefix = 0;
-  int want = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < n; j += kSelThreads) {
-      const uint32_t key = row_key(a, base, j, safe_from, has_safe);
-      if (shift == 24) {
-        if (key == 0u && isnan(a.s.weight[base + j])) report(a.status, SPATTEN_E_NONFINITE);
-        atomicAdd(&hist[key >> 24], 1);
-      } else if ((key >> (shift + 8)) == (prefix >> (shift + 8))) {
-        atomicAdd(&hist[(key >> shift) & 255u], 1);
-      }
-    }
-    __syncthreads();
-    if (tid < 32) {   // the bin that holds the want-th largest key: lane l sums bins 255-8l .. 248-8l
-      int c[8], sum = 0;
+  int32_t* from = a.from + bh * a.keep;
+  int moved = 0;
+  if (n > k) {
+    const bool has_safe = a.recent > 0;
+    const int safe_from = has_safe ? a.seen[b] - a.recent : 0;
+    int32_t *hole = a.hole + bh * a.m, *tail = a.tail + bh * a.m;
+    report_nan(a, base, n);
+    auto get = [&](int j) {
+      uint32_t key[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += (c[i] = hist[255 - 8 * tid - i]);
-      int inc = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (tid >= o) inc += x;
-      }
-      int before = inc - sum;
-      if (before < want && want <= inc) {
-        for (int i = 0; i < 8; ++i) {
-          if (want <= before + c[i]) {
-            s_prefix = prefix | static_cast<uint32_t>(255 - 8 * tid - i) << shift;
-            s_want = want - before;
-            break;
+      for (int u = 0; u < 4; ++u) key[u] = row_key(a, base, min(j + u, n - 1), safe_from, has_safe);
+      return make_uint4(key[0], key[1], key[2], key[3]);
+    };
+    const Threshold th = radix_select<kSelThreads>(n, k, get, hist, sums);
+    const bool in_place = a.in_place;
+    moved = rank_rows<kSelThreads>(
+        n, k, th, get, sums,
+        [&](int j, uint32_t holes, int i) {
+          for (int u = 0; u < 4; ++u) {
+            if ((holes >> u) & 1u) hole[i++] = j + u;
+            else if (!in_place && j + u < k) from[j + u] = j + u;
           }
-          before += c[i];
-        }
-      }
-    }
+        },
+        [&](int j, uint32_t tails, int i) {
+          for (int u = 0; u < 4; ++u)
+            if ((tails >> u) & 1u) tail[i++] = j + u;
+        });
     __syncthreads();
-    prefix = s_prefix;
-    want = s_want;
+    if (!a.in_place)
+      for (int i = tid; i < moved; i += kSelThreads) from[hole[i]] = tail[i];
+  } else if (!a.in_place) {
+    for (int i = tid; i < n; i += kSelThreads) from[i] = i;
   }
-  // rows with key > prefix stay; of those equal to it, the first `want`
-  int ties = 0, moved = 0;
-  int32_t* hole = a.hole + bh * a.m;
-  int32_t* tail = a.tail + bh * a.m;
-  int holes = 0, tails = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < n ? row_key(a, base, j, safe_from, has_safe) : 0u;
-    const bool tie = j < n && key == prefix;
-    int t0, t1;
-    const int2 tr = block_rank(tie, false, warp_sums, &t0, &t1);
-    const bool kept = j < n && (key > prefix || (tie && ties + tr.x < want));
-    ties += t0;
-    const bool is_hole = j < k && !kept, is_tail = j >= k && kept;
-    int h0, h1;
-    const int2 r = block_rank(is_hole, is_tail, warp_sums, &h0, &h1);
-    if (is_hole) hole[holes + r.x] = j;
-    if (is_tail) tail[tails + r.y] = j;
-    if (!a.in_place && j < k && kept) a.from[bh * a.keep + j] = j;
-    holes += h0;
-    tails += h1;
-  }
-  moved = holes;
-  __syncthreads();
-  if (!a.in_place)
-    for (int i = tid; i < moved; i += kSelThreads) a.from[bh * a.keep + hole[i]] = tail[i];
   if (tid == 0) {
-    a.count[2 * bh] = a.in_place ? moved : k;
-    a.count[2 * bh + 1] = k;
+    a.count[2 * bh] = a.in_place ? moved : min(n, k);
+    a.count[2 * bh + 1] = min(n, k);
   }
 }
 
-// Moves the planned rows: a row's codes are 16-byte pieces, its scales, weight and position one piece
-// each; consecutive lanes take the pieces of one row.
 template <int DH>
 __global__ void __launch_bounds__(kThreads) kv4_move_kernel(EvictArgs a) {
-  constexpr int kCode = DH / 32;            // 16-byte pieces of one tensor's codes
-  constexpr int kPieces = DH == 64 ? 8 : 16;   // lanes per row (128 channels: 12 in use)
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * a.s.H_kv + h;
   const int n = a.count[2 * bh];
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.len_out[b] = a.count[2 * bh + 1];
-  const int piece = threadIdx.x % kPieces;
-  for (int i = blockIdx.x * (kThreads / kPieces) + threadIdx.x / kPieces; i < n; i += gridDim.x * (kThreads / kPieces)) {
-    const int64_t from = bh * a.s.cap + (a.in_place ? a.tail[bh * a.m + i] : a.from[bh * a.keep + i]);
-    const int64_t to = bh * a.d.cap + (a.in_place ? a.hole[bh * a.m + i] : i);
-    if (piece < kCode) {
-      reinterpret_cast<uint4*>(a.d.k_codes)[to * kCode + piece] = reinterpret_cast<const uint4*>(a.s.k_codes)[from * kCode + piece];
-    } else if (piece < 2 * kCode) {
-      reinterpret_cast<uint4*>(a.d.v_codes)[to * kCode + piece - kCode] =
-          reinterpret_cast<const uint4*>(a.s.v_codes)[from * kCode + piece - kCode];
-    } else if (piece < 2 * kCode + 2) {
-      const uint16_t* s = piece == 2 * kCode ? a.s.k_scale : a.s.v_scale;
-      uint16_t* d = piece == 2 * kCode ? a.d.k_scale : a.d.v_scale;
-      if constexpr (DH == 64) reinterpret_cast<uint32_t*>(d)[to] = reinterpret_cast<const uint32_t*>(s)[from];
-      else reinterpret_cast<uint2*>(d)[to] = reinterpret_cast<const uint2*>(s)[from];
-    } else if (piece == 2 * kCode + 2) {
-      a.d.weight[to] = a.s.weight[from];
-    } else if (piece == 2 * kCode + 3) {
-      if (a.s.pos) a.d.pos[to] = a.s.pos[from];
-    }
-  }
+  move_rows<DH>(a, bh * a.s.cap, bh * a.d.cap, n, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads, [&](int i, int& to, int& from) {
+                  to = a.in_place ? a.hole[bh * a.m + i] : i;
+                  from = a.in_place ? a.tail[bh * a.m + i] : a.from[bh * a.keep + i];
+                });
 }
 
 bool same_cache(const spatten_kv4_cache& a, const spatten_kv4_cache& b) {
@@ -581,6 +826,12 @@ bool any_shared(const spatten_kv4_cache& a, const spatten_kv4_cache& b) {
   return a.k_codes == b.k_codes || a.k_scale == b.k_scale || a.v_codes == b.v_codes || a.v_scale == b.v_scale ||
          (a.weight && a.weight == b.weight) || (a.pos && a.pos == b.pos);
 }
+
+// shared memory of the one-launch kernel: keys and lists (17 KB of static arrays besides)
+size_t evict_shared(int32_t n_max, int32_t keep, int32_t m) {
+  return 4 * (align_up(n_max, 4) + align_up(m, 4) + align_up(keep > m ? keep : m, 4));
+}
+constexpr size_t kEvictShared = 208 * 1024;
 
 size_t evict_layout(const spatten_kv4_cache& c, int32_t n_max, int32_t keep, void* ws, size_t ws_bytes, EvictArgs* out) {
   WsCursor cur(ws, ws_bytes);
@@ -598,6 +849,52 @@ size_t evict_layout(const spatten_kv4_cache& c, int32_t n_max, int32_t keep, voi
     out->m = m;
   }
   return align_up(cur.used, 256);
+}
+
+template <int DH, int THREADS>
+int32_t evict_one_launch(const EvictArgs& a, int C, size_t shared, cudaStream_t st) {
+  static DeviceOnce once;
+  int dev;
+  SPT_TRY(once_per_device(once, &dev, [](int) -> int32_t {
+    SPT_CUDA(cudaFuncSetAttribute(kv4_evict_kernel<DH, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kEvictShared)));
+    return SPATTEN_OK;
+  }));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(C), static_cast<unsigned>(a.s.H_kv), static_cast<unsigned>(a.s.B));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SPT_CUDA(cudaLaunchKernelEx(&cfg, kv4_evict_kernel<DH, THREADS>, a));
+  SPT_TRY(launch_status());
+  if (a.len_out != a.len) return SPATTEN_OK;
+  kv4_evict_counts_kernel<<<static_cast<unsigned>(ceil_div(a.s.B, kThreads)), kThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+template <int DH>
+int32_t evict_launch(const EvictArgs& a, cudaStream_t st) {
+  const int64_t rows = a.in_place ? a.m : a.keep, pairs = static_cast<int64_t>(a.s.B) * a.s.H_kv;
+  const size_t shared = evict_shared(a.n_max, a.keep, a.m);
+  if (shared <= kEvictShared) {
+    // more CTAs while SMs are free and each has rows enough to move; large ones where one has an SM to itself
+    int C = 1;
+    while (C < 8 && pairs * C * 2 <= sm_count() && rows >= 256 * C) C *= 2;
+    return pairs * C <= sm_count() && a.n_max > 2048 ? evict_one_launch<DH, 1024>(a, C, shared, st)
+                                                     : evict_one_launch<DH, 512>(a, C, shared, st);
+  }
+  kv4_select_kernel<<<dim3(a.s.H_kv, a.s.B), kSelThreads, 0, st>>>(a);
+  SPT_TRY(launch_status());
+  // a few rows per thread group when there are many
+  const int per_block = kThreads / (DH / 16);
+  const int64_t want = ceil_div(rows, per_block), most = ceil_div(8 * sm_count(), pairs);
+  kv4_move_kernel<DH><<<dim3(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), a.s.H_kv, a.s.B), kThreads, 0, st>>>(a);
+  return launch_status();
 }
 
 }  // namespace
@@ -678,15 +975,5 @@ extern "C" int32_t spatten_kv4_evict(const spatten_kv4_cache* src, const spatten
   if (!a.in_place && any_shared(*src, *dst)) return SPATTEN_E_ARG;
   if (!ws || ws_bytes < evict_layout(*src, n_max, keep, ws, ws_bytes, &a)) return SPATTEN_E_WORKSPACE;
   if (!aligned16(ws)) return SPATTEN_E_ALIGN;
-  cudaStream_t st = as_stream(stream);
-  kv4_select_kernel<<<dim3(src->H_kv, src->B), kSelThreads, 0, st>>>(a);
-  SPT_TRY(launch_status());
-  // in place at most m rows move, else `keep`; a few rows per thread group when there are many
-  const int64_t rows = a.in_place ? a.m : keep;
-  const int per_block = kThreads / (src->d_h == 64 ? 8 : 16);
-  const int64_t want = ceil_div(rows, per_block), most = ceil_div(8 * 148, static_cast<int64_t>(src->B) * src->H_kv);
-  const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), src->H_kv, src->B);
-  if (src->d_h == 64) kv4_move_kernel<64><<<grid, kThreads, 0, st>>>(a);
-  else kv4_move_kernel<128><<<grid, kThreads, 0, st>>>(a);
-  return launch_status();
+  return src->d_h == 64 ? evict_launch<64>(a, as_stream(stream)) : evict_launch<128>(a, as_stream(stream));
 }

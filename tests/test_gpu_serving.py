@@ -593,3 +593,32 @@ def test_attention_scores_in_the_workspace(cuda, dtype, d):
     e = score_step(host(q)[0], k[0], n[0])
     check_out(host(o)[0], ref, spread, e, dtype, UBF if dtype == BF else 2 * U32)
     check_weight(host(c.t["weight"])[0], host(w0)[0], w, e)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_more_rows_than_shared_memory_holds(cuda, in_place):
+    """60,000 rows: the selection reads the weights themselves; many rows of one weight."""
+    S = lib()
+    n, keep, recent, d = [60000, 59999], 30001, 77, 64
+    cap = 60000
+    c = Cache(S, 2, 1, d, cap, seed=5)
+    r = np.random.default_rng(1)
+    w = np.zeros((2, 1, cap), np.float32)
+    w[0] = r.exponential(1, (1, cap))
+    w[1, 0, ::3] = 1.0
+    pos = np.tile(np.arange(cap, dtype=np.int32), (2, 1, 1))
+    c.t["weight"].copy_(torch.from_numpy(w))
+    c.t["pos"].copy_(torch.from_numpy(pos))
+    before = c.host()
+    dst = c if in_place else Cache(S, 2, 1, d, keep, seed=1)
+    ln, status = i32(n), i32([0])
+    lo = ln if in_place else torch.zeros_like(ln)
+    nb = S.kv4_evict_workspace_size(c.c, cap, keep)
+    S.kv4_evict(c.c, dst.c, ln, lo, i32(n), cap, keep, recent, ws(nb), nb, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and lo.tolist() == [keep, keep]
+    got = dst.host()
+    for b in range(2):
+        src = R.evict_sources(w[b, 0], pos[b, 0], n[b], n[b], keep, recent)
+        for k in before:
+            np.testing.assert_array_equal(got[k][b, 0, :keep], before[k][b, 0, src], err_msg=k)
