@@ -3,7 +3,8 @@
 // Two kernels, and a small third one when several query heads share a key/value head:
 //  OUTPUT  one pass over the visible keys in tiles of 128 with the running maximum and sum of the
 //          softmax.  A CTA owns NQ tiles of 128 query rows that read the same key/value head; each has
-//          a softmax warpgroup (thread r = TMEM lane r = row r), next to one TMA producer warp and one
+//          eight softmax warps (TMEM lane = row; two threads a row, 64 keys of a tile each, so that
+//          four warps a sub-core hide each other's latencies), next to one TMA producer warp and one
 //          MMA warp.  S = Q K^T goes to TMEM, P (bfloat16) goes back over the columns of S and is the
 //          TMEM operand of O += P V, so P never touches shared memory.
 //  WEIGHT  weight_j = sum_i exp(S_ij - m_i) / l_i needs final statistics, hence a second pass over the
@@ -40,8 +41,31 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
   else return make_float2(ex2(x.x), ex2(x.y));
 }
 
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// whether p holds in any of the 256 threads of a tile's softmax warps (named barrier id)
+__device__ __forceinline__ bool group_any(bool p, int id) {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "setp.ne.u32 p, %1, 0;\n"
+      "bar.red.or.pred q, %2, 256, p;\n"
+      "selp.u32 %0, 1, 0, q;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"(p ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// A wait of a whole warp: the first poll does not block, so that a limit of one poll is no wait at all.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t limit) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, limit));
+  bool ok = mbar_test_wait(bar, parity);
+  if (!ok) {
+    if (limit > 1) ok = wait_bar(bar, parity, abort_flag, limit - 1);
+    else *abort_flag = 1;
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // all of a [128 rows x DH] tile: one box per 64 channels
@@ -51,23 +75,46 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
   for (int c = 0; c < DH / 64; ++c) tma_load_3d(dst + c * kKT * 128, map, c * 64, head, row, bar);
 }
 
+// The MMA warp runs its loop as a whole and elects a lane (the same one every time) for the instructions
+// themselves: so operands are known to be uniform and stay in uniform registers.  Issued from a branch of
+// one lane, every MMA waited some 100 cycles for its operands to be moved there, against 64 of work.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  if (elect_one()) mma_commit(bar);
+}
+
+// Descriptors of a tile's first step; a later one adds its offset, in units of 16 bytes, to the address in the
+// low bits.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) { return desc_sw128(saddr, 16, 1024); }             // K-major
+__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr) { return desc_sw128(saddr, kKT * 128u, 1024); }     // MN-major
+
 // D[128 x 128] = A B^T over DH channels, both tiles K-major
 template <int DH>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t sA, uint32_t sB) {
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b) {
   constexpr uint32_t id = idesc_bf16(128, 128, false, false);
 #pragma unroll
   for (int s = 0; s < DH / 16; ++s) {
-    const uint32_t off = (s >> 2) * (kKT * 128u) + (s & 3) * 32u;
-    mma_f16(d, desc_sw128(sA + off, 16, 1024), desc_sw128(sB + off, 16, 1024), id, s > 0 ? 1u : 0u);
+    const uint32_t off = ((s >> 2) * (kKT * 128u) + (s & 3) * 32u) >> 4;
+    if (elect_one()) mma_f16(d, a + off, b + off, id, s > 0 ? 1u : 0u);
   }
 }
-// O (+)= P V: P in TMEM (8 columns per 16 keys), V rows MN-major
+// O (+)= P V: P in TMEM (8 columns per 16 keys, the second 64 keys 64 columns on), V rows MN-major
 template <int DH>
-__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint32_t sV, uint32_t acc) {
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t acc) {
   constexpr uint32_t id = idesc_bf16(128, DH, false, true);
 #pragma unroll
   for (int s = 0; s < static_cast<int>(kKT) / 16; ++s)
-    mma_f16_ts(d, p + s * 8, desc_sw128(sV + s * 2048u, kKT * 128u, 1024), id, (acc || s > 0) ? 1u : 0u);
+    if (elect_one()) mma_f16_ts(d, p + (s & 3) * 8 + (s >> 2) * 64, v + s * (2048u >> 4), id, (acc || s > 0) ? 1u : 0u);
 }
 
 struct Maps {
@@ -80,11 +127,11 @@ struct Maps {
 template <int DH_, int NQ_>
 struct OutCfg {
   static constexpr int DH = DH_, NQ = NQ_;
-  static constexpr int kStages = 5;                      // K and V tiles in flight, one ring
+  static constexpr int kStages = NQ == 1 ? 5 : 4;        // K and V tiles in flight, one ring
   static constexpr uint32_t kTile = kKT * DH * 2u;
   static constexpr uint32_t oKV = NQ * kTile;
   static constexpr uint32_t kSmem = oKV + kStages * kTile + 1024u;
-  static constexpr int kThreads = NQ * 128 + 64;
+  static constexpr int kThreads = NQ * 256 + 64;
   static constexpr uint32_t kTmem = NQ * (128 + DH) <= 256 ? 256 : 512;
   static constexpr int kCtas = kTmem == 256 ? 2 : 1;     // per SM
   static constexpr uint32_t tS = 0, tO = NQ * 128;
@@ -101,11 +148,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ OutBars<NQ, NST> bars;
+  __shared__ float row_stat[NQ][2][kKT];   // what the two halves of a row tell each other
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const spatten_prompt_args& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = a.H / a.H_kv;
   // NQ = 2: two heads of a group at the same rows, or (odd groups) 256 rows of one head
   const bool pair_heads = NQ == 2 && (G & 1) == 0;
@@ -129,8 +177,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   }
   const int partial = kr.n < Tmax * static_cast<int>(kKT) ? Tmax - 1 : -1;   // the tile that ends past the keys
 
-  constexpr int kProducer = 4 * NQ, kMma = 4 * NQ + 1;
-  if (warp == kMma) tmem_alloc(&tmem_base, C::kTmem);
+  constexpr int kProducer = 8 * NQ, kMma = 8 * NQ + 1;
+  if (warp == kMma) {
+    tmem_alloc(&tmem_base, C::kTmem);
+    tmem_relinquish();   // without it no second CTA becomes resident
+  }
   if (tid == 0) {
     abort_word = 0;
     mbar_init(&bars.q_full, 1);
@@ -140,7 +191,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     }
     for (int g = 0; g < NQ; ++g) {
       mbar_init(&bars.s_full[g], 1);
-      mbar_init(&bars.p_ready[g], 128);
+      mbar_init(&bars.p_ready[g], 256);
       mbar_init(&bars.o_full[g], 1);
     }
     mbar_init(&bars.v_fix, 32);
@@ -150,7 +201,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  const uint32_t tmem = tmem_base, wlim = p.wait_limit;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), wlim = p.wait_limit;
   bool aborted = false;
 
   if (warp == kProducer) {
@@ -194,21 +245,22 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.kv_full[x % NST], (x / NST) & 1);
     }
   } else if (warp == kMma) {
-    if (lane == 0 && Tmax > 0) {
+    if (Tmax > 0) {
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!aborted && !wait_bar(bar, parity, abort_flag, wlim)) aborted = true;
+        if (!aborted && !warp_wait(bar, parity, abort_flag, wlim)) aborted = true;
         return !aborted;
       };
-      const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::oKV);
+      const uint64_t dQ = desc_rows(smem_u32(smem)), dK = desc_rows(smem_u32(smem + C::oKV)), dV = desc_cols(smem_u32(smem + C::oKV));
+      constexpr uint32_t kStep = C::kTile >> 4;
       if (wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0)) {
         tc_after_sync();
 #pragma unroll
         for (int g = 0; g < NQ; ++g)
           if (T[g] > 0) {
-            mma_scores<DH>(tmem + C::tS + g * 128, sQ + g * C::kTile, sKV);
-            mma_commit(&bars.s_full[g]);
+            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dK);
+            commit_one(&bars.s_full[g]);
           }
-        mma_commit(&bars.kv_empty[0]);
+        commit_one(&bars.kv_empty[0]);
       }
       for (int t = 0; t < Tmax && !aborted; ++t) {
         const int xv = 2 * t + 1, xk = 2 * t + 2, sv = xv % NST, sk = xk % NST;
@@ -218,92 +270,107 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           if (!wait(&bars.p_ready[g], t & 1) || !wait(&bars.kv_full[sv], (xv / NST) & 1)) break;
           if (t == partial && !wait(&bars.v_fix, 0)) break;
           tc_after_sync();
-          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, sKV + sv * C::kTile, t > 0 ? 1u : 0u);
+          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, dV + sv * kStep, t > 0 ? 1u : 0u);
           if (t + 1 < T[g]) {
             if (!wait(&bars.kv_full[sk], (xk / NST) & 1)) break;
             tc_after_sync();
-            mma_scores<DH>(tmem + C::tS + g * 128, sQ + g * C::kTile, sKV + sk * C::kTile);
-            mma_commit(&bars.s_full[g]);
+            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dK + sk * kStep);
+            commit_one(&bars.s_full[g]);
           } else {
-            mma_commit(&bars.o_full[g]);
+            commit_one(&bars.o_full[g]);
           }
         }
         if (aborted) break;
-        mma_commit(&bars.kv_empty[sv]);
-        if (t + 1 < Tmax) mma_commit(&bars.kv_empty[sk]);
+        commit_one(&bars.kv_empty[sv]);
+        if (t + 1 < Tmax) commit_one(&bars.kv_empty[sk]);
       }
       if (aborted) {   // every MMA already issued completes before TMEM is freed
-        mma_commit(&bars.drain);
+        commit_one(&bars.drain);
         drain_wait(&bars.drain, 0);
       }
     }
     __syncwarp();
   } else {
-    const int g = NQ == 1 ? 0 : warp >> 2, r = tid & 127;
+    // warps 8 g + 4 half + quadrant: 32 rows, and 64 of the tile's keys
+    const int g = NQ == 1 ? 0 : warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
     const int my_row0 = g ? row0[NQ - 1] : row0[0], my_rows = g ? rows[NQ - 1] : rows[0], my_T = g ? T[NQ - 1] : T[0];
     const int my_head = g ? head[NQ - 1] : head[0];
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's TMEM lanes (32 (warp & 3)) << 16
-    const uint32_t tS = tmem + lanes + C::tS + g * 128, tO = tmem + lanes + C::tO + g * DH;
+    const uint32_t tS = tmem + lanes + C::tS + g * 128 + half * 64, tO = tmem + lanes + C::tO + g * DH + half * (DH / 2);
     const int last = my_row0 + r + shift;   // the last key this row sees
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
-    float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum
+    float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum of this half
     for (int t = 0; t < my_T; ++t) {
-      if (!warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim)) {
-        aborted = true;
-        break;
-      }
+      const bool ok = warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim);
       tc_after_sync();
-      float v[128];
+      const int j0 = t * static_cast<int>(kKT) + half * 64, lim = min(last, kr.n - 1) - j0;   // columns 0 .. lim are seen
+      const bool masked = j0 + 63 > my_row0 + shift || j0 + 64 > kr.n;
+      float mx = -INFINITY;
+      if (ok) {
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, v + ch * 32);
-      tmem_ld_wait();
-      const int j0 = t * static_cast<int>(kKT);
-      const bool masked = j0 + static_cast<int>(kKT) - 1 > my_row0 + shift || j0 + static_cast<int>(kKT) > kr.n;
-      if (masked) {
-        const int lim = min(last, kr.n - 1) - j0;
+        for (int ch = 0; ch < 2; ++ch) {   // the scores are read twice: registers for both halves would be too many
+          float v[32];
+          tmem_ld32(tS + ch * 32, v);
+          tmem_ld_wait();
+          if (masked) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) v[j] = j <= lim ? v[j] : -INFINITY;
+            for (int j = 0; j < 32; ++j) v[j] = ch * 32 + j <= lim ? v[j] : -INFINITY;
+          }
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[k] = v[k];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) x[k] = fmaxf(x[k], v[k + 4 * j]);
+          }
+          mx = fmaxf(mx, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+        }
       }
-      float mx[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        mx[k] = v[k];
-#pragma unroll
-        for (int j = 1; j < 16; ++j) mx[k] = fmaxf(mx[k], v[k + 8 * j]);
-      }
-      const float mt = c * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-      if (t == 0) {
-        m = mt;
-      } else if (__any_sync(0xffffffffu, mt > m + kRescale)) {
-        // the score MMA of this tile was issued behind the previous P V, so O is complete here
-        const float mn = fmaxf(m, mt);
+      const float mt = c * mx;
+      const bool grown = group_any(t == 0 || !ok || mt > m + kRescale, 1 + g);
+      if (grown) {
+        if (group_any(!ok, 1 + g)) {
+          aborted = true;
+          break;
+        }
+        row_stat[g][half][r] = mt;
+        named_sync(1 + g, 256);
+        const float mn = fmaxf(m, fmaxf(mt, row_stat[g][half ^ 1][r]));
         const float f = ex2(m - (mn == -INFINITY ? 0.0f : mn));
         m = mn;
         l *= f;
+        // the score MMA of this tile was issued behind the previous P V, so O is complete here
+        if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-        for (int ch = 0; ch < DH / 32; ++ch) {
-          float o[32];
-          tmem_ld32(tO + ch * 32, o);
-          tmem_ld_wait();
-          uint32_t u[32];
+          for (int ch = 0; ch < DH / 64; ++ch) {
+            float o[32];
+            tmem_ld32(tO + ch * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * f);
-          tmem_st16(tO + ch * 32, u);
-          tmem_st16(tO + ch * 32 + 16, u + 16);
+            for (int q = 0; q < 2; ++q) {
+              uint32_t u[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[16 * q + j] * f);
+              tmem_st16(tO + ch * 32 + 16 * q, u);
+            }
+          }
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
       const float2 nb = make_float2(-base, -base);
       float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
+      for (int ch = 0; ch < 2; ++ch) {
         uint32_t u[16];
+        float v[32];
+        tmem_ld32(tS + ch * 32, v);
+        tmem_ld_wait();
         if (masked) {   // the polynomial does not reach 0, which hidden keys need
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 x = __ffma2_rn(make_float2(v[ch * 32 + 2 * j], v[ch * 32 + 2 * j + 1]), cc, nb);
-            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            const float2 x = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), cc, nb);
+            const float2 e = make_float2(ch * 32 + 2 * j <= lim ? ex2(x.x) : 0.0f, ch * 32 + 2 * j + 1 <= lim ? ex2(x.y) : 0.0f);
             if (j & 1) s1 = __fadd2_rn(s1, e);
             else s0 = __fadd2_rn(s0, e);
             u[j] = pack_bf16x2(e.x, e.y);
@@ -311,7 +378,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         } else {
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const float* w = v + ch * 32 + 2 * j;
+            const float* w = v + 2 * j;
             const float2 e0 = exp2_pair<0>(__ffma2_rn(make_float2(w[0], w[1]), cc, nb));
             const float2 e1 = exp2_pair<1>(__ffma2_rn(make_float2(w[2], w[3]), cc, nb));
             const float2 e2 = exp2_pair<2>(__ffma2_rn(make_float2(w[4], w[5]), cc, nb));
@@ -324,12 +391,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
             u[j + 3] = pack_bf16x2(e3.x, e3.y);
           }
         }
-        tmem_st16(tS + ch * 16, u);
+        tmem_st16(tS + ch * 16, u);   // over this thread's own scores, read before
       }
       l += (s0.x + s1.x) + (s0.y + s1.y);
       tmem_st_wait();
       tc_before_sync();
       mbar_arrive(&bars.p_ready[g]);
+    }
+    if (!aborted) {   // the group agrees on that
+      named_sync(1 + g, 256);   // the maxima have been read
+      row_stat[g][half][r] = l;
+      named_sync(1 + g, 256);
+      l = row_stat[g][0][r] + row_stat[g][1][r];
     }
     // rows that see nothing have l = 0 and O = 0; a NaN sum stays one
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
@@ -337,9 +410,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     if (!aborted) {
       tc_after_sync();
       const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * (DH / 2));
 #pragma unroll 1
-      for (int ch = 0; ch < DH / 32; ++ch) {
+      for (int ch = 0; ch < DH / 64; ++ch) {
         float o[32];
         if (my_T > 0) {
           tmem_ld32(tO + ch * 32, o);
@@ -355,7 +428,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
                                          pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
         }
       }
-      if (p.stat_m && r < my_rows) {
+      if (p.stat_m && half == 0 && r < my_rows) {
         const int64_t at = static_cast<int64_t>(my_head) * a.total_q + row;
         p.stat_m[at] = m == -INFINITY ? 0.0f : -m;
         p.stat_l[at] = inv;
@@ -401,7 +474,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const spatten_prompt_args& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // tiles from the front: early keys are seen by the most rows
   const SeqTile st = find_seq_tile<true>(a.cu_kv, a.B, a.total_kv, kKT, blockIdx.x / a.H);
   if (st.b < 0) return;
@@ -412,7 +485,10 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
 
   constexpr int kProducer = 8, kMma = 9;
-  if (warp == kMma) tmem_alloc(&tmem_base, C::kTmem);
+  if (warp == kMma) {
+    tmem_alloc(&tmem_base, C::kTmem);
+    tmem_relinquish();   // without it no second CTA becomes resident
+  }
   if (tid == 0) {
     abort_word = 0;
     mbar_init(&bars.k_full, 1);
@@ -430,7 +506,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  const uint32_t tmem = tmem_base, wlim = p.wait_limit;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), wlim = p.wait_limit;
   bool aborted = false;
   float total = 0.0f;
 
@@ -472,23 +548,23 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.q_full[x % NST], (x / NST) & 1);
     }
   } else if (warp == kMma) {
-    if (lane == 0 && NT > 0) {
-      const uint32_t sK = smem_u32(smem);
-      if (!wait_bar(&bars.k_full, 0, abort_flag, wlim)) aborted = true;
+    if (NT > 0) {
+      const uint64_t dK = desc_rows(smem_u32(smem));
+      if (!warp_wait(&bars.k_full, 0, abort_flag, wlim)) aborted = true;
       for (int t = 0; t < NT && !aborted; ++t) {
         const int s = t % NST;
-        if (!wait_bar(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
-            !wait_bar(&bars.s_empty[t & 1], ((t >> 1) & 1) ^ 1u, abort_flag, wlim)) {
+        if (!warp_wait(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
+            !warp_wait(&bars.s_empty[t & 1], ((t >> 1) & 1) ^ 1u, abort_flag, wlim)) {
           aborted = true;
           break;
         }
         tc_after_sync();
-        mma_scores<DH>(tmem + (t & 1) * 128, sK, sK + (1 + s) * C::kTile);
-        mma_commit(&bars.s_full[t & 1]);
-        mma_commit(&bars.q_empty[s]);
+        mma_scores<DH>(tmem + (t & 1) * 128, dK, dK + (1 + s) * (C::kTile >> 4));
+        commit_one(&bars.s_full[t & 1]);
+        commit_one(&bars.q_empty[s]);
       }
       if (aborted) {
-        mma_commit(&bars.drain);
+        commit_one(&bars.drain);
         drain_wait(&bars.drain, 0);
       }
     }
