@@ -37,10 +37,9 @@ size_t layout(const spatten_prompt_args& a, void* ws, size_t ws_bytes, PromptPro
   WsCursor c(ws, ws_bytes);
   const size_t rows = static_cast<size_t>(a.H) * a.total_q;
   if (use_tc(a)) {
-    float* m = c.take<float>(rows);
-    float* l = c.take<float>(rows);
+    float* offset = c.take<float>(rows);
     float* part = a.H > a.H_kv ? c.take<float>(static_cast<size_t>(a.H) * a.total_kv) : nullptr;
-    if (p) p->stat_m = m, p->stat_l = l, p->part = part;
+    if (p) p->offset = offset, p->part = part;
   } else {
     float2* stats = c.take<float2>(rows);
     if (p) p->stats = stats;

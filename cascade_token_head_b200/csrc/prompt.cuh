@@ -8,11 +8,10 @@ namespace spt {
 struct PromptProblem {
   spatten_prompt_args a;   // sm_scale > 0 and cu_kv set
   // with weights only (else NULL).  CUDA cores: [H][total_q] score maximum (log2 units) and exponential
-  // sum of each row.  Tensor cores: the negated maximum and the reciprocal of the sum (0 where a row
-  // sees nothing) in two planes [H][total_q], and the heads' column sums [H][total_kv] (grouped heads).
+  // sum of each row.  Tensor cores: [H][total_q] what each row's scores need added (before the softmax
+  // scale) for their exponentials to be P, and [H][total_kv] the heads' column sums (grouped heads).
   float2* stats;
-  float* stat_m;
-  float* stat_l;
+  float* offset;
   float* part;
   uint32_t wait_limit;     // polls of one pipeline wait (tensor-core kernels)
 };

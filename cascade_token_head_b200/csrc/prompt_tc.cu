@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         if (!aborted && !warp_wait(bar, parity, abort_flag, wlim)) aborted = true;
         return !aborted;
       };
-      const uint64_t dQ = desc_rows(smem_u32(smem)), dK = desc_rows(smem_u32(smem + C::oKV)), dV = desc_cols(smem_u32(smem + C::oKV));
       constexpr uint32_t kStep = C::kTile >> 4;
+      const uint64_t dQ = desc_rows(smem_u32(smem)), dK = desc_rows(smem_u32(smem + C::oKV)), dV = desc_cols(smem_u32(smem + C::oKV));
       if (wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0)) {
         tc_after_sync();
 #pragma unroll
@@ -262,19 +262,22 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           }
         commit_one(&bars.kv_empty[0]);
       }
+      // One tile's P V and next scores run while the other tile's softmax does.  Between two tiles' MMAs there
+      // is only the wait for P: the tensor cores idle meanwhile.  (An MMA warp per tile was slower, 675 us
+      // against 519: the tiles' MMAs then alternate in the pipe.)
+      int sv = 1, sk = 2 % NST, pv = 0, pk = 0;   // the ring's stages of V(t) and K(t + 1), and their phases
       for (int t = 0; t < Tmax && !aborted; ++t) {
-        const int xv = 2 * t + 1, xk = 2 * t + 2, sv = xv % NST, sk = xk % NST;
+        const bool more = t + 1 < Tmax;
+        if (!wait(&bars.kv_full[sv], pv) || (t == partial && !wait(&bars.v_fix, 0)) || (more && !wait(&bars.kv_full[sk], pk))) break;
+        const uint64_t dVt = dV + sv * kStep, dKt = dK + sk * kStep;
 #pragma unroll
         for (int g = 0; g < NQ; ++g) {
           if (t >= T[g]) continue;
-          if (!wait(&bars.p_ready[g], t & 1) || !wait(&bars.kv_full[sv], (xv / NST) & 1)) break;
-          if (t == partial && !wait(&bars.v_fix, 0)) break;
+          if (!wait(&bars.p_ready[g], t & 1)) break;
           tc_after_sync();
-          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, dV + sv * kStep, t > 0 ? 1u : 0u);
+          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, dVt, t > 0 ? 1u : 0u);
           if (t + 1 < T[g]) {
-            if (!wait(&bars.kv_full[sk], (xk / NST) & 1)) break;
-            tc_after_sync();
-            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dK + sk * kStep);
+            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dKt);   // over the P that the MMAs before it read
             commit_one(&bars.s_full[g]);
           } else {
             commit_one(&bars.o_full[g]);
@@ -282,7 +285,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         }
         if (aborted) break;
         commit_one(&bars.kv_empty[sv]);
-        if (t + 1 < Tmax) commit_one(&bars.kv_empty[sk]);
+        if (more) commit_one(&bars.kv_empty[sk]);
+        if ((sv += 2) >= NST) sv -= NST, pv ^= 1;
+        if ((sk += 2) >= NST) sk -= NST, pk ^= 1;
       }
       if (aborted) {   // every MMA already issued completes before TMEM is freed
         commit_one(&bars.drain);
@@ -428,11 +433,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
                                          pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
         }
       }
-      if (p.stat_m && half == 0 && r < my_rows) {
-        const int64_t at = static_cast<int64_t>(my_head) * a.total_q + row;
-        p.stat_m[at] = m == -INFINITY ? 0.0f : -m;
-        p.stat_l[at] = inv;
-      }
+      if (p.offset && half == 0 && r < my_rows)   // exp2(c (S + offset)) = P
+        p.offset[static_cast<int64_t>(my_head) * a.total_q + row] = l > 0.0f ? -(m + log2f(l)) / c : (l == 0.0f ? 0.0f : l);
     }
   }
   tc_before_sync();
@@ -451,11 +453,28 @@ template <int DH_>
 struct WeightCfg {
   static constexpr int DH = DH_;
   static constexpr int kStages = DH == 64 ? 3 : 2;
-  static constexpr uint32_t kTile = kKT * DH * 2u;
-  static constexpr uint32_t kSmem = (1 + kStages) * kTile + 1024u;
+  static constexpr uint32_t kTile = kKT * DH * 2u, kExtra = kKT * 32u;   // and 16 channels more
+  static constexpr uint32_t oQ = kTile + kExtra, kStage = kTile + kExtra;
+  static constexpr uint32_t kSmem = oQ + kStages * kStage + 1024u;
   static constexpr int kSoftmax = 256, kThreads = kSoftmax + 64;
   static constexpr uint32_t kTmem = 256;   // two score buffers
 };
+
+// The row's offset -(m + log2 l) / c enters the scores by an MMA step of 16 channels more: the keys' are three
+// ones, the rows' the offset as the sum of three bfloat16 (24 bits).  So no thread reads a statistic, and a
+// weight costs a multiplication, an exponential and an addition.  32-byte rows, 32-byte swizzle.
+__device__ __forceinline__ uint32_t extra_at(uint32_t row, uint32_t chunk) {
+  return row * 32u + ((chunk ^ ((row >> 2) & 1u)) << 4);
+}
+__device__ __forceinline__ uint64_t desc_extra(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;   // 8-row groups
+  d |= static_cast<uint64_t>(1) << 46;          // descriptor version for tcgen05
+  d |= static_cast<uint64_t>(6) << 61;          // SWIZZLE_32B
+  return d;
+}
 
 template <int NST>
 struct WeightBars {
@@ -468,7 +487,6 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ WeightBars<NST> bars;
-  __shared__ __align__(16) float stat_m[NST][kKT], stat_l[NST][kKT];
   __shared__ float half_sum[kKT];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
@@ -485,6 +503,11 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
 
   constexpr int kProducer = 8, kMma = 9;
+  if (tid < static_cast<int>(kKT)) {   // the keys' extra channels: 1, 1, 1, 0, ..
+    *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 0)) = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+    *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
   if (warp == kMma) {
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();   // without it no second CTA becomes resident
@@ -494,7 +517,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     mbar_init(&bars.k_full, 1);
     for (int s = 0; s < NST; ++s) {
       mbar_init(&bars.q_full[s], 33);
-      mbar_init(&bars.q_empty[s], 9);
+      mbar_init(&bars.q_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
@@ -516,29 +539,35 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       mbar_arrive_expect_tx(&bars.k_full, C::kTile);
       load_tile<DH>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
     }
-    const int64_t at = static_cast<int64_t>(h) * a.total_q + qr.first;
+    const float* offset = p.offset + static_cast<int64_t>(h) * a.total_q + qr.first;
     for (int t = 0; t < NT; ++t) {
       const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
-      float sm[4], sl[4];
+      float v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {   // rows past the sequence are masked where they are used
         const int i = i0 + lane + 32 * k;
-        sm[k] = i < qr.n ? p.stat_m[at + i] : 0.0f;
-        sl[k] = i < qr.n ? p.stat_l[at + i] : 0.0f;
+        v[k] = i < qr.n ? offset[i] : 0.0f;
       }
       if (!warp_wait(&bars.q_empty[s], ((t / NST) & 1) ^ 1u, abort_flag, wlim)) {
         aborted = true;
         break;
       }
+      uint8_t* dst = smem + C::oQ + s * C::kStage;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars.q_full[s], C::kTile);
-        load_tile<DH>(smem + (1 + s) * C::kTile, &maps.q, h, qr.first + i0, &bars.q_full[s]);
+        load_tile<DH>(dst, &maps.q, h, qr.first + i0, &bars.q_full[s]);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        stat_m[s][lane + 32 * k] = sm[k];
-        stat_l[s][lane + 32 * k] = sl[k];
+        const uint32_t hi = pack_bf16x2(v[k], 0.0f);
+        const float r1 = v[k] - __uint_as_float(hi << 16);
+        const uint32_t mid = pack_bf16x2(r1, 0.0f);
+        const float r2 = r1 - __uint_as_float(mid << 16);
+        *reinterpret_cast<uint4*>(dst + C::kTile + extra_at(lane + 32 * k, 0)) =
+            make_uint4((hi & 0xffffu) | mid << 16, pack_bf16x2(r2, 0.0f), 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + C::kTile + extra_at(lane + 32 * k, 1)) = make_uint4(0u, 0u, 0u, 0u);
       }
+      fence_async_smem();
       mbar_arrive(&bars.q_full[s]);
       ++issued;
     }
@@ -549,7 +578,9 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     }
   } else if (warp == kMma) {
     if (NT > 0) {
-      const uint64_t dK = desc_rows(smem_u32(smem));
+      const uint64_t dK = desc_rows(smem_u32(smem)), dQ = desc_rows(smem_u32(smem + C::oQ));
+      const uint64_t eK = desc_extra(smem_u32(smem + C::kTile)), eQ = desc_extra(smem_u32(smem + C::oQ + C::kTile));
+      constexpr uint32_t id = idesc_bf16(128, 128, false, false);
       if (!warp_wait(&bars.k_full, 0, abort_flag, wlim)) aborted = true;
       for (int t = 0; t < NT && !aborted; ++t) {
         const int s = t % NST;
@@ -559,7 +590,8 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
           break;
         }
         tc_after_sync();
-        mma_scores<DH>(tmem + (t & 1) * 128, dK, dK + (1 + s) * (C::kTile >> 4));
+        mma_scores<DH>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
+        if (elect_one()) mma_f16(tmem + (t & 1) * 128, eK, eQ + s * (C::kStage >> 4), id, 1u);
         commit_one(&bars.s_full[t & 1]);
         commit_one(&bars.q_empty[s]);
       }
@@ -576,9 +608,8 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
     for (int t = 0; t < NT; ++t) {
-      const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
-      if (!warp_wait(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
-          !warp_wait(&bars.s_full[t & 1], (t >> 1) & 1, abort_flag, wlim)) {
+      const int i0 = (rt0 + t) * static_cast<int>(kKT);
+      if (!warp_wait(&bars.s_full[t & 1], (t >> 1) & 1, abort_flag, wlim)) {
         aborted = true;
         break;
       }
@@ -590,38 +621,27 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       tc_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
-      const float4* sm = reinterpret_cast<const float4*>(&stat_m[s][col0]);
-      const float4* sl = reinterpret_cast<const float4*>(&stat_l[s][col0]);
       float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
       if (i0 + static_cast<int>(kKT) <= qr.n && j0 + static_cast<int>(kKT) - 1 <= i0 + shift) {
 #pragma unroll
-        for (int q = 0; q < 16; q += 2) {
-          const float4 m0 = sm[q], l0 = sl[q], m1 = sm[q + 1], l1 = sl[q + 1];
-          const float* w = v + 4 * q;
-          s0 = __ffma2_rn(exp2_pair<0>(__ffma2_rn(make_float2(w[0], w[1]), cc, make_float2(m0.x, m0.y))), make_float2(l0.x, l0.y), s0);
-          s1 = __ffma2_rn(exp2_pair<1>(__ffma2_rn(make_float2(w[2], w[3]), cc, make_float2(m0.z, m0.w))), make_float2(l0.z, l0.w), s1);
-          s0 = __ffma2_rn(exp2_pair<2>(__ffma2_rn(make_float2(w[4], w[5]), cc, make_float2(m1.x, m1.y))), make_float2(l1.x, l1.y), s0);
-          s1 = __ffma2_rn(exp2_pair<3>(__ffma2_rn(make_float2(w[6], w[7]), cc, make_float2(m1.z, m1.w))), make_float2(l1.z, l1.w), s1);
+        for (int q = 0; q < 64; q += 8) {
+          const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
+          const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
+          const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
+          const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
+          s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
+          s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
         }
       } else {
         const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float4 m0 = sm[q], l0 = sl[q];
-          const float mm[4] = {m0.x, m0.y, m0.z, m0.w}, ll[4] = {l0.x, l0.y, l0.z, l0.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = 4 * q + k;
-            const float e = ex2(fmaf(v[col], c, mm[k])) * ll[k];
-            const float w = col >= lo && col < hi ? e : 0.0f;
-            if (k & 1) s1.x += w;
-            else s0.x += w;
-          }
+        for (int q = 0; q < 64; ++q) {
+          const float w = q >= lo && q < hi ? ex2(v[q] * c) : 0.0f;
+          if (q & 1) s1.x += w;
+          else s0.x += w;
         }
       }
       total += (s0.x + s1.x) + (s0.y + s1.y);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_empty[s]);
     }
     if (half) half_sum[(warp & 3) * 32 + lane] = total;
   }
