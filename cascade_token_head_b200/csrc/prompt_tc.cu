@@ -159,30 +159,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   const bool pair_heads = NQ == 2 && (G & 1) == 0;
   const int tile_rows = NQ == 2 && !pair_heads ? 256 : 128;
   const int slots = pair_heads ? a.H / 2 : a.H;
-  if (blockIdx.x == 0) report_bad_offsets(a);
-  const SeqTile st = find_seq_tile(a.cu_q, a.B, a.total_q, tile_rows, blockIdx.x / slots);
-  if (st.b < 0) return;
-  const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
-  const PackedRows qr = packed_rows(a.cu_q, st.b, a.total_q), kr = packed_rows(a.cu_kv, st.b, a.total_kv);
-  const int shift = kr.n - qr.n;
-  int head[NQ], row0[NQ], rows[NQ], T[NQ], Tmax = 0;
-#pragma unroll
-  for (int g = 0; g < NQ; ++g) {
-    head[g] = pair_heads ? 2 * slot + g : slot;
-    row0[g] = st.tile * tile_rows + (pair_heads ? 0 : 128 * g);
-    rows[g] = max(0, min(128, qr.n - row0[g]));
-    const int seen = rows[g] ? max(0, min(kr.n, row0[g] + rows[g] + shift)) : 0;   // keys the last row sees
-    T[g] = (seen + static_cast<int>(kKT) - 1) / static_cast<int>(kKT);
-    Tmax = max(Tmax, T[g]);
-  }
-  const int partial = kr.n < Tmax * static_cast<int>(kKT) ? Tmax - 1 : -1;   // the tile that ends past the keys
-
   constexpr int kProducer = 8 * NQ, kMma = 8 * NQ + 1;
   if (warp == kMma) {
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();   // without it no second CTA becomes resident
-  }
-  if (tid == 0) {
+  } else if (warp == kProducer && lane == 0) {
+    tma_prefetch_map(&maps.q);
+    tma_prefetch_map(&maps.k);
+    tma_prefetch_map(&maps.v);
     abort_word = 0;
     mbar_init(&bars.q_full, 1);
     for (int s = 0; s < NST; ++s) {
@@ -198,6 +182,44 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
+  if (blockIdx.x == 0) report_bad_offsets(a);
+  const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots);
+  if (pt.b < 0) {   // no such tile
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp == kMma) tmem_dealloc(tmem_base, C::kTmem);
+    return;
+  }
+  const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
+  const PackedRows qr = pt.q, kr = pt.k;
+  const int shift = kr.n - qr.n;
+  int head[NQ], row0[NQ], rows[NQ], T[NQ], Tmax = 0;
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) {
+    head[g] = pair_heads ? 2 * slot + g : slot;
+    row0[g] = pt.tile * tile_rows + (pair_heads ? 0 : 128 * g);
+    rows[g] = max(0, min(128, qr.n - row0[g]));
+    const int seen = rows[g] ? max(0, min(kr.n, row0[g] + rows[g] + shift)) : 0;   // keys the last row sees
+    T[g] = (seen + static_cast<int>(kKT) - 1) / static_cast<int>(kKT);
+    Tmax = max(Tmax, T[g]);
+  }
+  const int partial = kr.n < Tmax * static_cast<int>(kKT) ? Tmax - 1 : -1;   // the tile that ends past the keys
+
+  // the loads that wait for nothing, before the CTA meets
+  auto load_kv = [&](int x) {   // the ring's x-th tile: K0 V0 K1 V1 ..
+    mbar_arrive_expect_tx(&bars.kv_full[x % NST], C::kTile);
+    load_tile<DH>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, kr.first + (x >> 1) * static_cast<int>(kKT),
+                  &bars.kv_full[x % NST]);
+  };
+  const int early = min(NST, 2 * Tmax);
+  if (warp == kProducer && lane == 0 && Tmax > 0) {
+    mbar_arrive_expect_tx(&bars.q_full, NQ * C::kTile);
+#pragma unroll
+    for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
+      load_tile<DH>(smem + g * C::kTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
+    for (int x = 0; x < early; ++x) load_kv(x);
+  }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
@@ -205,27 +227,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   bool aborted = false;
 
   if (warp == kProducer) {
-    int issued = 0;
-    if (lane == 0 && Tmax > 0) {
-      mbar_arrive_expect_tx(&bars.q_full, NQ * C::kTile);
-#pragma unroll
-      for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
-        load_tile<DH>(smem + g * C::kTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
-    }
-    for (int x = 0; x < 2 * Tmax; ++x) {   // K0 V0 K1 V1 ...: the order in which the MMA warp uses them
+    int issued = early;
+    for (int x = 0; x < 2 * Tmax; ++x) {
       const int s = x % NST, t = x >> 1;
       const uint32_t ph = (x / NST) & 1;
-      if (!warp_wait(&bars.kv_empty[s], ph ^ 1u, abort_flag, wlim)) {
-        aborted = true;
-        break;
+      if (x >= early) {
+        if (!warp_wait(&bars.kv_empty[s], ph ^ 1u, abort_flag, wlim)) {
+          aborted = true;
+          break;
+        }
+        if (lane == 0) load_kv(x);
+        ++issued;
       }
-      uint8_t* dst = smem + C::oKV + s * C::kTile;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars.kv_full[s], C::kTile);
-        load_tile<DH>(dst, (x & 1) ? &maps.v : &maps.k, hk, kr.first + t * static_cast<int>(kKT), &bars.kv_full[s]);
-      }
-      ++issued;
       if ((x & 1) && t == partial) {
+        uint8_t* dst = smem + C::oKV + s * C::kTile;
         // rows past the sequence's keys meet P = 0: they must be finite, so they become zeros
         if (!warp_wait(&bars.kv_full[s], ph, abort_flag, wlim)) {
           aborted = true;
@@ -240,7 +255,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         mbar_arrive(&bars.v_fix);
       }
     }
-    if (aborted && lane == 0) {   // the copies in flight land before shared memory is given up
+    if (aborted && lane == 0 && Tmax > 0) {   // the copies in flight land before shared memory is given up
       drain_wait(&bars.q_full, 0);
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.kv_full[x % NST], (x / NST) & 1);
     }
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     const int my_head = g ? head[NQ - 1] : head[0];
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's TMEM lanes (32 (warp & 3)) << 16
     const uint32_t tS = tmem + lanes + C::tS + g * 128 + half * 64, tO = tmem + lanes + C::tO + g * DH + half * (DH / 2);
-    const int last = my_row0 + r + shift;   // the last key this row sees
+    const int last = my_row0 + r + shift, warp_last = my_row0 + (warp & 3) * 32 + shift;   // the last key this row sees, the warp's first one
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
     float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum of this half
@@ -310,15 +325,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       const bool ok = warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim);
       tc_after_sync();
       const int j0 = t * static_cast<int>(kKT) + half * 64, lim = min(last, kr.n - 1) - j0;   // columns 0 .. lim are seen
-      const bool masked = j0 + 63 > my_row0 + shift || j0 + 64 > kr.n;
+      // of 32 columns, whether every row of the warp sees all, or none any
+      const int lim_first = min(warp_last, kr.n - 1) - j0, lim_last = min(warp_last + 31, kr.n - 1) - j0;
       float mx = -INFINITY;
       if (ok) {
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {   // the scores are read twice: registers for both halves would be too many
+          if (lim_last < ch * 32) continue;
           float v[32];
           tmem_ld32(tS + ch * 32, v);
           tmem_ld_wait();
-          if (masked) {
+          if (lim_first < ch * 32 + 31) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = ch * 32 + j <= lim ? v[j] : -INFINITY;
           }
@@ -369,9 +386,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       for (int ch = 0; ch < 2; ++ch) {
         uint32_t u[16];
         float v[32];
-        tmem_ld32(tS + ch * 32, v);
-        tmem_ld_wait();
-        if (masked) {   // the polynomial does not reach 0, which hidden keys need
+        if (lim_last >= ch * 32) {
+          tmem_ld32(tS + ch * 32, v);
+          tmem_ld_wait();
+        }
+        if (lim_last < ch * 32) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = 0u;
+        } else if (lim_first < ch * 32 + 31) {   // the polynomial does not reach 0, which hidden keys need
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float2 x = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), cc, nb);
@@ -493,38 +515,49 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   volatile int* abort_flag = &abort_word;
   const spatten_prompt_args& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  // tiles from the front: early keys are seen by the most rows
-  const SeqTile st = find_seq_tile<true>(a.cu_kv, a.B, a.total_kv, kKT, blockIdx.x / a.H);
-  if (st.b < 0) return;
-  const int h = blockIdx.x % a.H, G = a.H / a.H_kv, hk = h / G;
-  const PackedRows qr = packed_rows(a.cu_q, st.b, a.total_q), kr = packed_rows(a.cu_kv, st.b, a.total_kv);
-  const int j0 = st.tile * static_cast<int>(kKT), shift = kr.n - qr.n;
-  const int rt0 = max(0, j0 - shift) / static_cast<int>(kKT);   // the first row tile that sees key j0
-  const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
-
   constexpr int kProducer = 8, kMma = 9;
-  if (tid < static_cast<int>(kKT)) {   // the keys' extra channels: 1, 1, 1, 0, ..
+  if (warp == kMma) {
+    tmem_alloc(&tmem_base, C::kTmem);
+    tmem_relinquish();   // without it no second CTA becomes resident
+  } else if (warp == kProducer) {
+    if (lane == 0) {
+      tma_prefetch_map(&maps.q);
+      tma_prefetch_map(&maps.k);
+      abort_word = 0;
+      mbar_init(&bars.k_full, 1);
+      for (int s = 0; s < NST; ++s) {
+        mbar_init(&bars.q_full[s], 33);
+        mbar_init(&bars.q_empty[s], 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bars.s_full[s], 1);
+        mbar_init(&bars.s_empty[s], 8);
+      }
+      mbar_init(&bars.drain, 1);
+      fence_mbar_init();
+    }
+  } else if (tid < static_cast<int>(kKT)) {   // the keys' extra channels: 1, 1, 1, 0, ..
     *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 0)) = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
     *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
-  if (warp == kMma) {
-    tmem_alloc(&tmem_base, C::kTmem);
-    tmem_relinquish();   // without it no second CTA becomes resident
+  const PromptTile pt = find_prompt_tile<true>(a, kKT, blockIdx.x / a.H);
+  if (pt.b < 0) {   // no such tile
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp == kMma) tmem_dealloc(tmem_base, C::kTmem);
+    return;
   }
-  if (tid == 0) {
-    abort_word = 0;
-    mbar_init(&bars.k_full, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&bars.q_full[s], 33);
-      mbar_init(&bars.q_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.s_empty[s], 8);
-    }
-    mbar_init(&bars.drain, 1);
-    fence_mbar_init();
+  const int h = blockIdx.x % a.H, G = a.H / a.H_kv, hk = h / G;
+  const PackedRows qr = pt.q, kr = pt.k;
+  const int j0 = pt.tile * static_cast<int>(kKT), shift = kr.n - qr.n;
+  const int rt0 = max(0, j0 - shift) / static_cast<int>(kKT);   // the first row tile that sees key j0
+  const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
+
+  if (warp == kProducer && lane == 0 && NT > 0) {   // the keys, before the CTA meets
+    mbar_arrive_expect_tx(&bars.k_full, C::kTile);
+    load_tile<DH>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
   }
   tc_before_sync();
   __syncthreads();
@@ -535,10 +568,6 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
 
   if (warp == kProducer) {
     int issued = 0;
-    if (lane == 0 && NT > 0) {
-      mbar_arrive_expect_tx(&bars.k_full, C::kTile);
-      load_tile<DH>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
-    }
     const float* offset = p.offset + static_cast<int64_t>(h) * a.total_q + qr.first;
     for (int t = 0; t < NT; ++t) {
       const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
@@ -622,23 +651,29 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
       float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-      if (i0 + static_cast<int>(kKT) <= qr.n && j0 + static_cast<int>(kKT) - 1 <= i0 + shift) {
+      const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
+      const int lo_first = lo - lane, lo_last = lo_first + 31;       // of the warp's first and last key
 #pragma unroll
-        for (int q = 0; q < 64; q += 8) {
-          const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
-          const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
-          const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
-          const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
-          s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
-          s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
-        }
-      } else {
-        const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
+      for (int ch = 0; ch < 2; ++ch) {
+        const float* w = v + ch * 32;
+        if (lo_first >= ch * 32 + 32 || hi <= ch * 32) continue;     // no column sees any of the keys
+        if (lo_last <= ch * 32 && hi >= ch * 32 + 32) {
 #pragma unroll
-        for (int q = 0; q < 64; ++q) {
-          const float w = q >= lo && q < hi ? ex2(v[q] * c) : 0.0f;
-          if (q & 1) s1.x += w;
-          else s0.x += w;
+          for (int q = 0; q < 32; q += 8) {
+            const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(w[q], w[q + 1]), cc));
+            const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(w[q + 2], w[q + 3]), cc));
+            const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(w[q + 4], w[q + 5]), cc));
+            const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(w[q + 6], w[q + 7]), cc));
+            s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
+            s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const float e = ch * 32 + q >= lo && ch * 32 + q < hi ? ex2(w[q] * c) : 0.0f;
+            if (q & 1) s1.x += e;
+            else s0.x += e;
+          }
         }
       }
       total += (s0.x + s1.x) + (s0.y + s1.y);
@@ -654,7 +689,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     if (G > 1) {
       p.part[static_cast<int64_t>(h) * a.total_kv + kr.first + j] = sum;
     } else if (j < a.weight_cap) {
-      a.weight[static_cast<int64_t>(st.b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
+      a.weight[static_cast<int64_t>(pt.b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
     } else {
       report(a.dev_status, SPATTEN_E_INDEX);
     }
