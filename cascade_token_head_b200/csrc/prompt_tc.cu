@@ -31,7 +31,8 @@ namespace {
 using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kKT = 128;          // keys per tile, query rows per tile
+constexpr int kRows = 128;             // rows of a query tile (and, for the weights, keys of a key tile)
+constexpr int kBox = 64;               // rows of a TMA box
 constexpr float kRescale = 8.0f;       // growth of a row's maximum (log2) that makes O be rescaled
 
 // 2^x of a pair; pair Q of every four takes the FMA pipe when Q < 1
@@ -42,18 +43,18 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
 }
 
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-// whether p holds in any of the 256 threads of a tile's softmax warps (named barrier id)
-__device__ __forceinline__ bool group_any(bool p, int id) {
+// whether p holds in any of the threads that share a named barrier
+__device__ __forceinline__ bool group_any(bool p, int id, int threads) {
   uint32_t r;
   asm volatile(
       "{\n"
       ".reg .pred p, q;\n"
       "setp.ne.u32 p, %1, 0;\n"
-      "bar.red.or.pred q, %2, 256, p;\n"
+      "bar.red.or.pred q, %2, %3, p;\n"
       "selp.u32 %0, 1, 0, q;\n"
       "}\n"
       : "=r"(r)
-      : "r"(p ? 1u : 0u), "r"(id)
+      : "r"(p ? 1u : 0u), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -68,11 +69,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// all of a [128 rows x DH] tile: one box per 64 channels
-template <int DH>
+// all of a [ROWS x DH] tile: blocks of 64 channels, each the rows' 128 bytes one behind the other
+template <int DH, int ROWS>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, uint64_t* bar) {
 #pragma unroll
-  for (int c = 0; c < DH / 64; ++c) tma_load_3d(dst + c * kKT * 128, map, c * 64, head, row, bar);
+  for (int c = 0; c < DH / 64; ++c)
+#pragma unroll
+    for (int r = 0; r < ROWS; r += kBox) tma_load_3d(dst + (c * ROWS + r) * 128, map, c * 64, head, row + r, bar);
 }
 
 // The MMA warp runs its loop as a whole and elects a lane (the same one every time) for the instructions
@@ -96,24 +99,25 @@ __device__ __forceinline__ void commit_one(uint64_t* bar) {
 // Descriptors of a tile's first step; a later one adds its offset, in units of 16 bytes, to the address in the
 // low bits.
 __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) { return desc_sw128(saddr, 16, 1024); }             // K-major
-__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr) { return desc_sw128(saddr, kKT * 128u, 1024); }     // MN-major
+template <int ROWS>
+__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr) { return desc_sw128(saddr, ROWS * 128u, 1024); }    // MN-major
 
-// D[128 x 128] = A B^T over DH channels, both tiles K-major
-template <int DH>
+// D[128 x N] = A B^T over DH channels, both tiles K-major
+template <int DH, int N>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t id = idesc_bf16(128, N, false, false);
 #pragma unroll
   for (int s = 0; s < DH / 16; ++s) {
-    const uint32_t off = ((s >> 2) * (kKT * 128u) + (s & 3) * 32u) >> 4;
-    if (elect_one()) mma_f16(d, a + off, b + off, id, s > 0 ? 1u : 0u);
+    const uint32_t at = ((s >> 2) * (kRows * 128u) + (s & 3) * 32u) >> 4, bt = ((s >> 2) * (N * 128u) + (s & 3) * 32u) >> 4;
+    if (elect_one()) mma_f16(d, a + at, b + bt, id, s > 0 ? 1u : 0u);
   }
 }
 // O (+)= P V: P in TMEM (8 columns per 16 keys, the second 64 keys 64 columns on), V rows MN-major
-template <int DH>
+template <int DH, int KT>
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t acc) {
   constexpr uint32_t id = idesc_bf16(128, DH, false, true);
 #pragma unroll
-  for (int s = 0; s < static_cast<int>(kKT) / 16; ++s)
+  for (int s = 0; s < KT / 16; ++s)
     if (elect_one()) mma_f16_ts(d, p + (s & 3) * 8 + (s >> 2) * 64, v + s * (2048u >> 4), id, (acc || s > 0) ? 1u : 0u);
 }
 
@@ -124,17 +128,20 @@ struct Maps {
 // =================================================================================================
 // OUTPUT
 // =================================================================================================
-template <int DH_, int NQ_>
+// NQ query tiles a CTA, tiles of KT keys.  One thread has a row and 64 keys of each tile; where a tile has 128
+// keys the two threads of a row share its maximum.
+template <int DH_, int NQ_, int KT_, int STAGES>
 struct OutCfg {
-  static constexpr int DH = DH_, NQ = NQ_;
-  static constexpr int kStages = NQ == 1 ? 5 : 4;        // K and V tiles in flight, one ring
-  static constexpr uint32_t kTile = kKT * DH * 2u;
-  static constexpr uint32_t oKV = NQ * kTile;
+  static constexpr int DH = DH_, NQ = NQ_, KT = KT_, kHalves = KT / 64;
+  static constexpr int kStages = STAGES;                 // K and V tiles in flight, one ring
+  static constexpr uint32_t kQTile = kRows * DH * 2u, kTile = KT * DH * 2u;
+  static constexpr uint32_t oKV = NQ * kQTile;
   static constexpr uint32_t kSmem = oKV + kStages * kTile + 1024u;
-  static constexpr int kThreads = NQ * 256 + 64;
-  static constexpr uint32_t kTmem = NQ * (128 + DH) <= 256 ? 256 : 512;
-  static constexpr int kCtas = kTmem == 256 ? 2 : 1;     // per SM
-  static constexpr uint32_t tS = 0, tO = NQ * 128;
+  static constexpr int kGroup = 128 * kHalves;           // softmax threads of a query tile
+  static constexpr int kThreads = NQ * kGroup + 64;
+  static constexpr uint32_t kColumns = NQ * (KT + DH), kTmem = kColumns <= 128 ? 128 : (kColumns <= 256 ? 256 : 512);
+  static constexpr int kCtas = 512 / kTmem;              // per SM
+  static constexpr uint32_t tS = 0, tO = NQ * KT;
 };
 
 template <int NQ, int NST>
@@ -144,11 +151,11 @@ struct OutBars {
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
-  constexpr int DH = C::DH, NQ = C::NQ, NST = C::kStages;
+  constexpr int DH = C::DH, NQ = C::NQ, KT = C::KT, NST = C::kStages, kHalves = C::kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ OutBars<NQ, NST> bars;
-  __shared__ float row_stat[NQ][2][kKT];   // what the two halves of a row tell each other
+  __shared__ float row_stat[NQ][kHalves][kRows];   // what the two halves of a row tell each other
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
@@ -159,7 +166,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   const bool pair_heads = NQ == 2 && (G & 1) == 0;
   const int tile_rows = NQ == 2 && !pair_heads ? 256 : 128;
   const int slots = pair_heads ? a.H / 2 : a.H;
-  constexpr int kProducer = 8 * NQ, kMma = 8 * NQ + 1;
+  constexpr int kProducer = NQ * C::kGroup / 32, kMma = kProducer + 1;
   if (warp == kMma) {
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();   // without it no second CTA becomes resident
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     }
     for (int g = 0; g < NQ; ++g) {
       mbar_init(&bars.s_full[g], 1);
-      mbar_init(&bars.p_ready[g], 256);
+      mbar_init(&bars.p_ready[g], C::kGroup);
       mbar_init(&bars.o_full[g], 1);
     }
     mbar_init(&bars.v_fix, 32);
@@ -201,23 +208,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     row0[g] = pt.tile * tile_rows + (pair_heads ? 0 : 128 * g);
     rows[g] = max(0, min(128, qr.n - row0[g]));
     const int seen = rows[g] ? max(0, min(kr.n, row0[g] + rows[g] + shift)) : 0;   // keys the last row sees
-    T[g] = (seen + static_cast<int>(kKT) - 1) / static_cast<int>(kKT);
+    T[g] = (seen + KT - 1) / KT;
     Tmax = max(Tmax, T[g]);
   }
-  const int partial = kr.n < Tmax * static_cast<int>(kKT) ? Tmax - 1 : -1;   // the tile that ends past the keys
+  const int partial = kr.n < Tmax * KT ? Tmax - 1 : -1;   // the tile that ends past the keys
 
   // the loads that wait for nothing, before the CTA meets
   auto load_kv = [&](int x) {   // the ring's x-th tile: K0 V0 K1 V1 ..
     mbar_arrive_expect_tx(&bars.kv_full[x % NST], C::kTile);
-    load_tile<DH>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, kr.first + (x >> 1) * static_cast<int>(kKT),
+    load_tile<DH, KT>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, kr.first + (x >> 1) * KT,
                   &bars.kv_full[x % NST]);
   };
   const int early = min(NST, 2 * Tmax);
   if (warp == kProducer && lane == 0 && Tmax > 0) {
-    mbar_arrive_expect_tx(&bars.q_full, NQ * C::kTile);
+    mbar_arrive_expect_tx(&bars.q_full, NQ * C::kQTile);
 #pragma unroll
     for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
-      load_tile<DH>(smem + g * C::kTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
+      load_tile<DH, kRows>(smem + g * C::kQTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
     for (int x = 0; x < early; ++x) load_kv(x);
   }
   tc_before_sync();
@@ -246,11 +253,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           aborted = true;
           break;
         }
-        const int first = kr.n - t * static_cast<int>(kKT);
-        for (int e = first * 8 + lane; e < static_cast<int>(kKT) * 8; e += 32)
+        const int first = kr.n - t * KT;
+        for (int e = first * 8 + lane; e < KT * 8; e += 32)
 #pragma unroll
           for (int c = 0; c < DH / 64; ++c)
-            *reinterpret_cast<uint4*>(dst + c * kKT * 128 + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(dst + c * KT * 128 + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
         mbar_arrive(&bars.v_fix);
       }
@@ -266,13 +273,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         return !aborted;
       };
       constexpr uint32_t kStep = C::kTile >> 4;
-      const uint64_t dQ = desc_rows(smem_u32(smem)), dK = desc_rows(smem_u32(smem + C::oKV)), dV = desc_cols(smem_u32(smem + C::oKV));
+      const uint64_t dQ = desc_rows(smem_u32(smem)), dK = desc_rows(smem_u32(smem + C::oKV)), dV = desc_cols<KT>(smem_u32(smem + C::oKV));
       if (wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0)) {
         tc_after_sync();
 #pragma unroll
         for (int g = 0; g < NQ; ++g)
           if (T[g] > 0) {
-            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dK);
+            mma_scores<DH, KT>(tmem + C::tS + g * KT, dQ + g * (C::kQTile >> 4), dK);
             commit_one(&bars.s_full[g]);
           }
         commit_one(&bars.kv_empty[0]);
@@ -290,9 +297,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           if (t >= T[g]) continue;
           if (!wait(&bars.p_ready[g], t & 1)) break;
           tc_after_sync();
-          mma_pv<DH>(tmem + C::tO + g * DH, tmem + C::tS + g * 128, dVt, t > 0 ? 1u : 0u);
+          mma_pv<DH, KT>(tmem + C::tO + g * DH, tmem + C::tS + g * KT, dVt, t > 0 ? 1u : 0u);
           if (t + 1 < T[g]) {
-            mma_scores<DH>(tmem + C::tS + g * 128, dQ + g * kStep, dKt);   // over the P that the MMAs before it read
+            mma_scores<DH, KT>(tmem + C::tS + g * KT, dQ + g * (C::kQTile >> 4), dKt);   // over the P that the MMAs before it read
             commit_one(&bars.s_full[g]);
           } else {
             commit_one(&bars.o_full[g]);
@@ -311,70 +318,84 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     }
     __syncwarp();
   } else {
-    // warps 8 g + 4 half + quadrant: 32 rows, and 64 of the tile's keys
-    const int g = NQ == 1 ? 0 : warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
+    // warp (tile g, half, quadrant): 32 rows, and 64 of a tile's keys
+    const int g = NQ == 1 ? 0 : warp / (4 * kHalves), half = kHalves == 1 ? 0 : (warp >> 2) & 1, r = tid & 127;
     const int my_row0 = g ? row0[NQ - 1] : row0[0], my_rows = g ? rows[NQ - 1] : rows[0], my_T = g ? T[NQ - 1] : T[0];
     const int my_head = g ? head[NQ - 1] : head[0];
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's TMEM lanes (32 (warp & 3)) << 16
-    const uint32_t tS = tmem + lanes + C::tS + g * 128 + half * 64, tO = tmem + lanes + C::tO + g * DH + half * (DH / 2);
-    const int last = my_row0 + r + shift, warp_last = my_row0 + (warp & 3) * 32 + shift;   // the last key this row sees, the warp's first one
+    constexpr int kOCols = DH / kHalves;                            // columns of O that this thread scales and stores
+    const uint32_t tS = tmem + lanes + C::tS + g * KT + half * 64, tO = tmem + lanes + C::tO + g * DH + half * kOCols;
+    // the last key that this row sees, and that the warp's first one does
+    const int last = min(my_row0 + r + shift, kr.n - 1), warp_row = my_row0 + (warp & 3) * 32;
+    const int last_first = min(warp_row + shift, kr.n - 1), last_last = min(warp_row + 31 + shift, kr.n - 1);
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
     float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum of this half
     for (int t = 0; t < my_T; ++t) {
       const bool ok = warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim);
       tc_after_sync();
-      const int j0 = t * static_cast<int>(kKT) + half * 64, lim = min(last, kr.n - 1) - j0;   // columns 0 .. lim are seen
-      // of 32 columns, whether every row of the warp sees all, or none any
-      const int lim_first = min(warp_last, kr.n - 1) - j0, lim_last = min(warp_last + 31, kr.n - 1) - j0;
+      const int j0 = t * KT + half * 64, lim = last - j0;   // columns 0 .. lim are seen
+      const bool full = last_first - j0 >= 63;              // by every row of the warp
       float mx = -INFINITY;
-      if (ok) {
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {   // the scores are read twice: registers for both halves would be too many
-          if (lim_last < ch * 32) continue;
-          float v[32];
-          tmem_ld32(tS + ch * 32, v);
+      if (ok) {   // the scores are read twice: there are not registers enough to keep them over the vote
+        if (full) {
+          float v[64];
+          tmem_ld32(tS, v);
+          tmem_ld32(tS + 32, v + 32);
           tmem_ld_wait();
-          if (lim_first < ch * 32 + 31) {
+          float x[8];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = ch * 32 + j <= lim ? v[j] : -INFINITY;
-          }
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 8; ++k) {
             x[k] = v[k];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) x[k] = fmaxf(x[k], v[k + 4 * j]);
+            for (int j = 1; j < 8; ++j) x[k] = fmaxf(x[k], v[k + 8 * j]);
           }
-          mx = fmaxf(mx, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+          mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < 64 && last_last - j0 >= ch; ch += 32) {
+            float v[32];
+            tmem_ld32(tS + ch, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, ch + j <= lim ? v[j] : -INFINITY);
+          }
         }
       }
       const float mt = c * mx;
-      const bool grown = group_any(t == 0 || !ok || mt > m + kRescale, 1 + g);
-      if (grown) {
-        if (group_any(!ok, 1 + g)) {
-          aborted = true;
-          break;
+      const bool grow = t == 0 || !ok || mt > m + kRescale;
+      if (kHalves == 1 ? __any_sync(0xffffffffu, grow) : group_any(grow, 1 + g, C::kGroup)) {
+        float mn = fmaxf(m, mt);
+        if constexpr (kHalves == 1) {
+          if (!ok) {
+            aborted = true;
+            break;
+          }
+        } else {
+          if (group_any(!ok, 1 + g, C::kGroup)) {   // the group agrees
+            aborted = true;
+            break;
+          }
+          row_stat[g][half][r] = mt;
+          named_sync(1 + g, C::kGroup);
+          mn = fmaxf(mn, row_stat[g][half ^ 1][r]);
         }
-        row_stat[g][half][r] = mt;
-        named_sync(1 + g, 256);
-        const float mn = fmaxf(m, fmaxf(mt, row_stat[g][half ^ 1][r]));
         const float f = ex2(m - (mn == -INFINITY ? 0.0f : mn));
         m = mn;
         l *= f;
         // the score MMA of this tile was issued behind the previous P V, so O is complete here
         if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-          for (int ch = 0; ch < DH / 64; ++ch) {
+          for (int ch = 0; ch < kOCols; ch += 32) {
             float o[32];
-            tmem_ld32(tO + ch * 32, o);
+            tmem_ld32(tO + ch, o);
             tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t u[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[16 * q + j] * f);
-              tmem_st16(tO + ch * 32 + 16 * q, u);
+              tmem_st16(tO + ch + 16 * q, u);
             }
           }
         }
@@ -382,27 +403,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       const float base = m == -INFINITY ? 0.0f : m;
       const float2 nb = make_float2(-base, -base);
       float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+      if (full) {
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        uint32_t u[16];
-        float v[32];
-        if (lim_last >= ch * 32) {
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t u[16];
+          float v[32];
           tmem_ld32(tS + ch * 32, v);
           tmem_ld_wait();
-        }
-        if (lim_last < ch * 32) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = 0u;
-        } else if (lim_first < ch * 32 + 31) {   // the polynomial does not reach 0, which hidden keys need
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), cc, nb);
-            const float2 e = make_float2(ch * 32 + 2 * j <= lim ? ex2(x.x) : 0.0f, ch * 32 + 2 * j + 1 <= lim ? ex2(x.y) : 0.0f);
-            if (j & 1) s1 = __fadd2_rn(s1, e);
-            else s0 = __fadd2_rn(s0, e);
-            u[j] = pack_bf16x2(e.x, e.y);
-          }
-        } else {
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float* w = v + 2 * j;
@@ -417,19 +424,40 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
             u[j + 2] = pack_bf16x2(e2.x, e2.y);
             u[j + 3] = pack_bf16x2(e3.x, e3.y);
           }
+          tmem_st16(tS + ch * 16, u);   // over this thread's own scores, read before
         }
-        tmem_st16(tS + ch * 16, u);   // over this thread's own scores, read before
+      } else {   // by ex2 alone: the polynomial does not reach 0, which hidden keys need
+#pragma unroll 1
+        for (int ch = 0; ch < 64; ch += 32) {
+          uint32_t u[16];
+          if (last_last - j0 >= ch) {
+            float v[32];
+            tmem_ld32(tS + ch, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), cc, nb);
+              const float2 e = make_float2(ch + 2 * j <= lim ? ex2(x.x) : 0.0f, ch + 2 * j + 1 <= lim ? ex2(x.y) : 0.0f);
+              s0 = __fadd2_rn(s0, e);
+              u[j] = pack_bf16x2(e.x, e.y);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = 0u;
+          }
+          tmem_st16(tS + (ch >> 1), u);
+        }
       }
       l += (s0.x + s1.x) + (s0.y + s1.y);
       tmem_st_wait();
       tc_before_sync();
       mbar_arrive(&bars.p_ready[g]);
     }
-    if (!aborted) {   // the group agrees on that
-      named_sync(1 + g, 256);   // the maxima have been read
+    if (kHalves == 2 && !aborted) {   // the group agrees on that
+      named_sync(1 + g, C::kGroup);   // the maxima have been read
       row_stat[g][half][r] = l;
-      named_sync(1 + g, 256);
-      l = row_stat[g][0][r] + row_stat[g][1][r];
+      named_sync(1 + g, C::kGroup);
+      l = row_stat[g][0][r] + row_stat[g][kHalves - 1][r];
     }
     // rows that see nothing have l = 0 and O = 0; a NaN sum stays one
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
@@ -437,9 +465,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     if (!aborted) {
       tc_after_sync();
       const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * (DH / 2));
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
 #pragma unroll 1
-      for (int ch = 0; ch < DH / 64; ++ch) {
+      for (int ch = 0; ch < kOCols / 32; ++ch) {
         float o[32];
         if (my_T > 0) {
           tmem_ld32(tO + ch * 32, o);
@@ -475,7 +503,7 @@ template <int DH_>
 struct WeightCfg {
   static constexpr int DH = DH_;
   static constexpr int kStages = DH == 64 ? 3 : 2;
-  static constexpr uint32_t kTile = kKT * DH * 2u, kExtra = kKT * 32u;   // and 16 channels more
+  static constexpr uint32_t kTile = kRows * DH * 2u, kExtra = kRows * 32u;   // and 16 channels more
   static constexpr uint32_t oQ = kTile + kExtra, kStage = kTile + kExtra;
   static constexpr uint32_t kSmem = oQ + kStages * kStage + 1024u;
   static constexpr int kSoftmax = 256, kThreads = kSoftmax + 64;
@@ -509,7 +537,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ WeightBars<NST> bars;
-  __shared__ float half_sum[kKT];
+  __shared__ float half_sum[kRows];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
@@ -536,12 +564,12 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       mbar_init(&bars.drain, 1);
       fence_mbar_init();
     }
-  } else if (tid < static_cast<int>(kKT)) {   // the keys' extra channels: 1, 1, 1, 0, ..
+  } else if (tid < kRows) {   // the keys' extra channels: 1, 1, 1, 0, ..
     *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 0)) = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
     *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
-  const PromptTile pt = find_prompt_tile<true>(a, kKT, blockIdx.x / a.H);
+  const PromptTile pt = find_prompt_tile<true>(a, kRows, blockIdx.x / a.H);
   if (pt.b < 0) {   // no such tile
     tc_before_sync();
     __syncthreads();
@@ -551,13 +579,13 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   }
   const int h = blockIdx.x % a.H, G = a.H / a.H_kv, hk = h / G;
   const PackedRows qr = pt.q, kr = pt.k;
-  const int j0 = pt.tile * static_cast<int>(kKT), shift = kr.n - qr.n;
-  const int rt0 = max(0, j0 - shift) / static_cast<int>(kKT);   // the first row tile that sees key j0
-  const int NT = max(0, (qr.n + static_cast<int>(kKT) - 1) / static_cast<int>(kKT) - rt0);
+  const int j0 = pt.tile * kRows, shift = kr.n - qr.n;
+  const int rt0 = max(0, j0 - shift) / kRows;   // the first row tile that sees key j0
+  const int NT = max(0, (qr.n + kRows - 1) / kRows - rt0);
 
   if (warp == kProducer && lane == 0 && NT > 0) {   // the keys, before the CTA meets
     mbar_arrive_expect_tx(&bars.k_full, C::kTile);
-    load_tile<DH>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
+    load_tile<DH, kRows>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
   }
   tc_before_sync();
   __syncthreads();
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     int issued = 0;
     const float* offset = p.offset + static_cast<int64_t>(h) * a.total_q + qr.first;
     for (int t = 0; t < NT; ++t) {
-      const int s = t % NST, i0 = (rt0 + t) * static_cast<int>(kKT);
+      const int s = t % NST, i0 = (rt0 + t) * kRows;
       float v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {   // rows past the sequence are masked where they are used
@@ -584,7 +612,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       uint8_t* dst = smem + C::oQ + s * C::kStage;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars.q_full[s], C::kTile);
-        load_tile<DH>(dst, &maps.q, h, qr.first + i0, &bars.q_full[s]);
+        load_tile<DH, kRows>(dst, &maps.q, h, qr.first + i0, &bars.q_full[s]);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -619,7 +647,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
           break;
         }
         tc_after_sync();
-        mma_scores<DH>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
+        mma_scores<DH, kRows>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
         if (elect_one()) mma_f16(tmem + (t & 1) * 128, eK, eQ + s * (C::kStage >> 4), id, 1u);
         commit_one(&bars.s_full[t & 1]);
         commit_one(&bars.q_empty[s]);
@@ -637,44 +665,50 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
     for (int t = 0; t < NT; ++t) {
-      const int i0 = (rt0 + t) * static_cast<int>(kKT);
+      const int i0 = (rt0 + t) * kRows;
       if (!warp_wait(&bars.s_full[t & 1], (t >> 1) & 1, abort_flag, wlim)) {
         aborted = true;
         break;
       }
       tc_after_sync();
-      float v[64];
-      tmem_ld32(tmem + lanes + (t & 1) * 128 + col0, v);
-      tmem_ld32(tmem + lanes + (t & 1) * 128 + col0 + 32, v + 32);
-      tmem_ld_wait();
-      tc_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
-      float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+      const uint32_t tS = tmem + lanes + (t & 1) * 128 + col0;
       const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
-      const int lo_first = lo - lane, lo_last = lo_first + 31;       // of the warp's first and last key
+      const int lo_first = lo - lane;                                // the same for the warp's first key
+      float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+      if (lo_first + 31 <= 0 && hi >= 64) {   // all of the warp's
+        float v[64];
+        tmem_ld32(tS, v);
+        tmem_ld32(tS + 32, v + 32);
+        tmem_ld_wait();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        const float* w = v + ch * 32;
-        if (lo_first >= ch * 32 + 32 || hi <= ch * 32) continue;     // no column sees any of the keys
-        if (lo_last <= ch * 32 && hi >= ch * 32 + 32) {
-#pragma unroll
-          for (int q = 0; q < 32; q += 8) {
-            const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(w[q], w[q + 1]), cc));
-            const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(w[q + 2], w[q + 3]), cc));
-            const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(w[q + 4], w[q + 5]), cc));
-            const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(w[q + 6], w[q + 7]), cc));
-            s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
-            s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
-          }
-        } else {
+        for (int q = 0; q < 64; q += 8) {
+          const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
+          const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
+          const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
+          const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
+          s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
+          s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
+        }
+      } else {
+#pragma unroll 1
+        for (int ch = 0; ch < 64; ch += 32) {
+          if (lo_first >= ch + 32 || hi <= ch) continue;   // none of the warp's
+          float v[32];
+          tmem_ld32(tS + ch, v);
+          tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
-            const float e = ch * 32 + q >= lo && ch * 32 + q < hi ? ex2(w[q] * c) : 0.0f;
+            const float e = ch + q >= lo && ch + q < hi ? ex2(v[q] * c) : 0.0f;
             if (q & 1) s1.x += e;
             else s0.x += e;
           }
         }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
       }
       total += (s0.x + s1.x) + (s0.y + s1.y);
     }
@@ -683,7 +717,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   tc_before_sync();
   const bool any_abort = __syncthreads_or(aborted);
   if (any_abort && tid == 0) report(a.dev_status, SPATTEN_E_TIMEOUT);
-  if (tid < static_cast<int>(kKT) && j0 + tid < kr.n) {
+  if (tid < kRows && j0 + tid < kr.n) {
     const float sum = any_abort ? 0.0f : total + half_sum[tid];
     const int j = j0 + tid;
     if (G > 1) {
@@ -740,13 +774,13 @@ EncodeFn encode_fn() {
   return reinterpret_cast<EncodeFn>(f);
 }
 
-// [rows][heads][DH] with a row stride of ld elements, read in boxes of 128 rows x 1 head x 64 channels
+// [rows][heads][DH] with a row stride of ld elements, read in boxes of 64 rows x 1 head x 64 channels
 int32_t make_map(CUtensorMap* m, const void* base, int dh, int heads, int rows, int64_t ld) {
   const EncodeFn enc = encode_fn();
   if (!enc) return SPATTEN_E_UNSUPPORTED;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dh) * 2, static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[3] = {64, 1, kKT}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, kBox}, step[3] = {1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -771,7 +805,7 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
   const int tile_rows = O::NQ == 2 && !pair_heads ? 256 : 128;
   // a sequence's rows end in at most one partial tile, so this many tiles cover any offsets
   const int64_t q_blocks = (static_cast<int64_t>(a.total_q) / tile_rows + a.B) * (pair_heads ? a.H / 2 : a.H);
-  const int64_t k_blocks = (static_cast<int64_t>(a.total_kv) / kKT + a.B) * a.H;
+  const int64_t k_blocks = (static_cast<int64_t>(a.total_kv) / kRows + a.B) * a.H;
   if (q_blocks > INT32_MAX || k_blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
   prompt_out_kernel<O><<<static_cast<unsigned>(q_blocks), O::kThreads, O::kSmem, st>>>(p, maps);
   SPT_TRY(launch_status());
@@ -791,8 +825,8 @@ bool prompt_tc_supported(const spatten_prompt_args& a) {
 }
 
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st) {
-  if (p.a.d_h == 64) return launch<OutCfg<64, 1>, WeightCfg<64>>(p, st);
-  return launch<OutCfg<128, 2>, WeightCfg<128>>(p, st);
+  if (p.a.d_h == 64) return launch<OutCfg<64, 1, 64, 4>, WeightCfg<64>>(p, st);
+  return launch<OutCfg<128, 2, 128, 4>, WeightCfg<128>>(p, st);
 }
 
 }  // namespace spt
