@@ -210,6 +210,8 @@ __device__ __forceinline__ BlockRows find_block_rows(const int32_t* cu, int B, i
 
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, bool counts) {
+  grid_dep_trigger();
+  grid_dep_wait();
   const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>;
   // the counts, where no other block still reads them (len_out and seen_out are buffers of their own)
   if (counts && blockIdx.y == 0)
@@ -254,6 +256,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, b
 
 // The counts of a call whose outputs are its inputs, after the rows.
 __global__ void __launch_bounds__(kThreads) kv4_counts_kernel(AppendArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   for (int s = blockIdx.x * kThreads + threadIdx.x; s < a.c.B; s += gridDim.x * kThreads) {
     const PackedRows p = packed_rows(a.cu, s, a.total);
     if (p.bad) report(a.status, SPATTEN_E_INDEX);
@@ -267,6 +271,8 @@ __global__ void __launch_bounds__(kThreads) kv4_counts_kernel(AppendArgs a) {
 // sequence's counts in place once its threads have read them.
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_token_kernel(AppendArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   constexpr int kLanes = DH / 8;
   const int b = blockIdx.x;
   const int row = clamp_len(a.len[b], a.c.cap, a.status);
@@ -307,19 +313,16 @@ __global__ void __launch_bounds__(kThreads) kv4_append_token_kernel(AppendArgs a
 template <int DH, typename T>
 int32_t append_launch(const AppendArgs& a, cudaStream_t st) {
   if (!a.cu) {
-    kv4_append_token_kernel<DH, T><<<a.c.B, kThreads, 0, st>>>(a);
-    return launch_status();
+    return launch_chained(kv4_append_token_kernel<DH, T>, dim3(a.c.B), dim3(kThreads), 0, st, 1, a);
   }
   const bool apart = a.len_out != a.len && (!a.seen_out || a.seen_out != a.seen);
   if (a.total > 0) {
     // a sequence's rows end in at most one partial run, so this many cover any offsets
     const dim3 grid(a.total / kBlockRows<DH> + a.c.B, a.c.H_kv);
-    kv4_append_kernel<DH, T><<<grid, kThreads, 0, st>>>(a, apart);
-    SPT_TRY(launch_status());
+    SPT_TRY(launch_chained(kv4_append_kernel<DH, T>, grid, dim3(kThreads), 0, st, 1, a, apart));
     if (apart) return SPATTEN_OK;
   }
-  kv4_counts_kernel<<<static_cast<unsigned>(ceil_div(a.c.B, kThreads)), kThreads, 0, st>>>(a);
-  return launch_status();
+  return launch_chained(kv4_counts_kernel, dim3(static_cast<unsigned>(ceil_div(a.c.B, kThreads))), dim3(kThreads), 0, st, 1, a);
 }
 
 // ----------------------------------------------------------------------------------------------
@@ -362,6 +365,8 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint3
 // memory: 16,384 rows of 16 heads of 64 to bfloat16 (86 MB) take <T_READ>.
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   constexpr int G = DH / kKv4Group;
   const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>, g = oct >> 2;
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -680,6 +685,8 @@ __device__ __forceinline__ void report_nan(const EvictArgs& a, int64_t base, int
 // The work per row is small: what is bounded is latency (radix passes and ranks: 5 us for 1152 rows).
 template <int DH, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_evict_kernel(EvictArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   extern __shared__ __align__(16) uint32_t keys[];   // [n_max] keys (to a multiple of 4), then the lists
   __shared__ int hist[kBins], sums[3][32];
   cg::cluster_group cluster = cg::this_cluster();
@@ -756,6 +763,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_evict_kernel(Evic
 }
 
 __global__ void __launch_bounds__(kThreads) kv4_evict_counts_kernel(EvictArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.s.B; b += gridDim.x * kThreads)
     a.len_out[b] = min(clamp_len(a.len[b], a.n_max, nullptr), a.keep);
 }
@@ -763,6 +772,8 @@ __global__ void __launch_bounds__(kThreads) kv4_evict_counts_kernel(EvictArgs a)
 // Caches whose keys and lists do not fit shared memory: one CTA per (sequence, head) selects from the weights
 // themselves and writes the moves to the workspace, a second launch moves.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(EvictArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   __shared__ int hist[kBins], sums[3][32];
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int64_t bh = static_cast<int64_t>(b) * a.s.H_kv + h, base = bh * a.s.cap;
@@ -808,6 +819,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(EvictArgs a) {
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads) kv4_move_kernel(EvictArgs a) {
+  grid_dep_trigger();
+  grid_dep_wait();
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * a.s.H_kv + h;
   const int n = a.count[2 * bh];
@@ -859,22 +872,9 @@ int32_t evict_one_launch(const EvictArgs& a, int C, size_t shared, cudaStream_t 
     SPT_CUDA(cudaFuncSetAttribute(kv4_evict_kernel<DH, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kEvictShared)));
     return SPATTEN_OK;
   }));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(C), static_cast<unsigned>(a.s.H_kv), static_cast<unsigned>(a.s.B));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  SPT_CUDA(cudaLaunchKernelEx(&cfg, kv4_evict_kernel<DH, THREADS>, a));
-  SPT_TRY(launch_status());
+  SPT_TRY(launch_chained(kv4_evict_kernel<DH, THREADS>, dim3(C, a.s.H_kv, a.s.B), dim3(THREADS), shared, st, C, a));
   if (a.len_out != a.len) return SPATTEN_OK;
-  kv4_evict_counts_kernel<<<static_cast<unsigned>(ceil_div(a.s.B, kThreads)), kThreads, 0, st>>>(a);
-  return launch_status();
+  return launch_chained(kv4_evict_counts_kernel, dim3(static_cast<unsigned>(ceil_div(a.s.B, kThreads))), dim3(kThreads), 0, st, 1, a);
 }
 
 template <int DH>
@@ -888,13 +888,12 @@ int32_t evict_launch(const EvictArgs& a, cudaStream_t st) {
     return pairs * C <= sm_count() && a.n_max > 2048 ? evict_one_launch<DH, 1024>(a, C, shared, st)
                                                      : evict_one_launch<DH, 512>(a, C, shared, st);
   }
-  kv4_select_kernel<<<dim3(a.s.H_kv, a.s.B), kSelThreads, 0, st>>>(a);
-  SPT_TRY(launch_status());
+  SPT_TRY(launch_chained(kv4_select_kernel, dim3(a.s.H_kv, a.s.B), dim3(kSelThreads), 0, st, 1, a));
   // a few rows per thread group when there are many
   const int per_block = kThreads / (DH / 16);
   const int64_t want = ceil_div(rows, per_block), most = ceil_div(8 * sm_count(), pairs);
-  kv4_move_kernel<DH><<<dim3(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), a.s.H_kv, a.s.B), kThreads, 0, st>>>(a);
-  return launch_status();
+  const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), a.s.H_kv, a.s.B);
+  return launch_chained(kv4_move_kernel<DH>, grid, dim3(kThreads), 0, st, 1, a);
 }
 
 }  // namespace
@@ -939,15 +938,10 @@ extern "C" int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* c
   if (total == 0) return SPATTEN_OK;
   const ReadArgs a{*c, cu, row0, total, {k_out, v_out}, ld_tok, dev_status};
   const dim3 grid(total / (c->d_h == 64 ? kBlockRows<64> : kBlockRows<128>) + c->B, c->H_kv);
-  cudaStream_t st = as_stream(stream);
-  if (c->d_h == 64) {
-    if (dtype == SPATTEN_BF16) kv4_read_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-    else kv4_read_kernel<64, float><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (dtype == SPATTEN_BF16) kv4_read_kernel<128, __nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-    else kv4_read_kernel<128, float><<<grid, kThreads, 0, st>>>(a);
-  }
-  return launch_status();
+  const bool bf = dtype == SPATTEN_BF16;
+  const auto kernel = c->d_h == 64 ? (bf ? kv4_read_kernel<64, __nv_bfloat16> : kv4_read_kernel<64, float>)
+                                   : (bf ? kv4_read_kernel<128, __nv_bfloat16> : kv4_read_kernel<128, float>);
+  return launch_chained(kernel, grid, dim3(kThreads), 0, as_stream(stream), 1, a);
 }
 
 extern "C" size_t spatten_kv4_evict_workspace_size(const spatten_kv4_cache* src, int32_t n_max, int32_t keep) {

@@ -398,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   __shared__ float2 in_ml[kMaxC][kHeads];
   __shared__ float in_o[kHeads * DH];
   __shared__ float2 f[kHeads];                   // the cluster's maxima, and sums inverted
+  grid_dep_trigger();
+  grid_dep_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int C = gridDim.x, rank = blockIdx.x;
   const spatten_kv4_attn_args& a = args.a;
@@ -656,19 +658,8 @@ int32_t launch(const AttnArgs& x, const Shape& s, cudaStream_t st) {
                                   static_cast<int>(kSharedOne)));
     return SPATTEN_OK;
   }));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(s.C);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(s.C), static_cast<unsigned>(x.a.cache.H_kv), static_cast<unsigned>(x.a.cache.B));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring_bytes(DH, NH) + s.x_smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  SPT_CUDA(cudaLaunchKernelEx(&cfg, kv4_attn_kernel<DH, NH, T>, x));
-  return launch_status();
+  return launch_chained(kv4_attn_kernel<DH, NH, T>, dim3(s.C, x.a.cache.H_kv, x.a.cache.B), dim3(kThreads),
+                        ring_bytes(DH, NH) + s.x_smem, st, s.C, x);
 }
 
 template <int DH, typename T>

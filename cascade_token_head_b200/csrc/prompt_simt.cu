@@ -57,6 +57,8 @@ __device__ __forceinline__ void scores4(const PromptSmem<DH>& sm, int warp, int 
 
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptProblem p) {
+  grid_dep_trigger();
+  grid_dep_wait();
   extern __shared__ __align__(16) char smem_raw[];
   PromptSmem<DH>& sm = *reinterpret_cast<PromptSmem<DH>*>(smem_raw);
   constexpr int kC = DH / 32;   // channels per lane
@@ -131,6 +133,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptProblem p) 
 
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads) prompt_weight_simt_kernel(PromptProblem p) {
+  grid_dep_trigger();
+  grid_dep_wait();
   extern __shared__ __align__(16) char smem_raw[];
   PromptSmem<DH>& sm = *reinterpret_cast<PromptSmem<DH>*>(smem_raw);
   const spatten_prompt_args& a = p.a;
@@ -190,11 +194,9 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
   // a sequence's rows end in at most one partial tile, so this many tiles cover any offsets
   const int64_t q_tiles = a.total_q / kRows + a.B, k_tiles = a.total_kv / kKeys + a.B;
   if (q_tiles * a.H > INT32_MAX || k_tiles * a.H_kv > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
-  prompt_simt_kernel<DH, T><<<static_cast<unsigned>(q_tiles * a.H), kThreads, bytes, st>>>(p);
-  SPT_TRY(launch_status());
+  SPT_TRY(launch_chained(prompt_simt_kernel<DH, T>, dim3(static_cast<unsigned>(q_tiles * a.H)), dim3(kThreads), bytes, st, 1, p));
   if (!a.weight || a.total_kv == 0) return SPATTEN_OK;
-  prompt_weight_simt_kernel<DH, T><<<static_cast<unsigned>(k_tiles * a.H_kv), kThreads, bytes, st>>>(p);
-  return launch_status();
+  return launch_chained(prompt_weight_simt_kernel<DH, T>, dim3(static_cast<unsigned>(k_tiles * a.H_kv)), dim3(kThreads), bytes, st, 1, p);
 }
 
 }  // namespace

@@ -35,12 +35,14 @@ constexpr int kRows = 128;             // rows of a query tile (and, for the wei
 constexpr int kBox = 64;               // rows of a TMA box
 constexpr float kRescale = 8.0f;       // growth of a row's maximum (log2) that makes O be rescaled
 
-// 2^x of a pair; pair Q of every four takes the FMA pipe when Q < 1
-template <int Q>
+__device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+// the same by the FMA pipe for the first POLY of every four pairs (Q: the pair)
+template <int Q, int POLY>
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
-  if constexpr ((Q & 3) < 1) return exp2_poly2(x);
-  else return make_float2(ex2(x.x), ex2(x.y));
+  if constexpr ((Q & 3) < POLY) return exp2_poly2(x);
+  else return ex2_pair(x);
 }
+constexpr int kWeightPoly = 1;   // of the weights' exponentials (8192 tokens: 316 us; none 341, half 337)
 
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // whether p holds in any of the threads that share a named barrier
@@ -149,6 +151,26 @@ struct OutBars {
   uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[NQ], p_ready[NQ], o_full[NQ], v_fix, drain;
 };
 
+// What a CTA does with its tile.
+template <class C>
+struct OutWork {
+  int head[C::NQ], row0[C::NQ], rows[C::NQ], T[C::NQ];   // of each query tile: head, rows of the sequence, key tiles seen
+  int Tmax, partial;                                     // the most key tiles; the one that ends past the keys, or -1
+  __device__ __forceinline__ OutWork(const PromptTile& pt, int slot, bool pair_heads, int tile_rows) {
+    Tmax = 0;
+#pragma unroll
+    for (int g = 0; g < C::NQ; ++g) {
+      head[g] = pair_heads ? 2 * slot + g : slot;
+      row0[g] = pt.tile * tile_rows + (pair_heads ? 0 : 128 * g);
+      rows[g] = max(0, min(128, pt.q.n - row0[g]));
+      const int seen = rows[g] ? max(0, min(pt.k.n, row0[g] + rows[g] + pt.k.n - pt.q.n)) : 0;   // keys the last row sees
+      T[g] = (seen + C::KT - 1) / C::KT;
+      Tmax = max(Tmax, T[g]);
+    }
+    partial = pt.k.n < Tmax * C::KT ? Tmax - 1 : -1;
+  }
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
   constexpr int DH = C::DH, NQ = C::NQ, KT = C::KT, NST = C::kStages, kHalves = C::kHalves;
@@ -157,6 +179,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   __shared__ OutBars<NQ, NST> bars;
   __shared__ float row_stat[NQ][kHalves][kRows];   // what the two halves of a row tell each other
   __shared__ uint32_t tmem_base;
+  __shared__ PromptTile item;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const spatten_prompt_args& a = p.a;
@@ -189,48 +212,46 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
+  grid_dep_trigger();
+  grid_dep_wait();
   if (blockIdx.x == 0) report_bad_offsets(a);
-  const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots);
-  if (pt.b < 0) {   // no such tile
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    if (warp == kMma) tmem_dealloc(tmem_base, C::kTmem);
-    return;
-  }
+  // one warp looks the tile up and starts the loads that wait for nothing, before the CTA meets
   const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
-  const PackedRows qr = pt.q, kr = pt.k;
-  const int shift = kr.n - qr.n;
-  int head[NQ], row0[NQ], rows[NQ], T[NQ], Tmax = 0;
-#pragma unroll
-  for (int g = 0; g < NQ; ++g) {
-    head[g] = pair_heads ? 2 * slot + g : slot;
-    row0[g] = pt.tile * tile_rows + (pair_heads ? 0 : 128 * g);
-    rows[g] = max(0, min(128, qr.n - row0[g]));
-    const int seen = rows[g] ? max(0, min(kr.n, row0[g] + rows[g] + shift)) : 0;   // keys the last row sees
-    T[g] = (seen + KT - 1) / KT;
-    Tmax = max(Tmax, T[g]);
-  }
-  const int partial = kr.n < Tmax * KT ? Tmax - 1 : -1;   // the tile that ends past the keys
-
-  // the loads that wait for nothing, before the CTA meets
-  auto load_kv = [&](int x) {   // the ring's x-th tile: K0 V0 K1 V1 ..
+  auto load_kv = [&](int x, int first) {   // the ring's x-th tile: K0 V0 K1 V1 ..
     mbar_arrive_expect_tx(&bars.kv_full[x % NST], C::kTile);
-    load_tile<DH, KT>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, kr.first + (x >> 1) * KT,
-                  &bars.kv_full[x % NST]);
+    load_tile<DH, KT>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, first + (x >> 1) * KT, &bars.kv_full[x % NST]);
   };
-  const int early = min(NST, 2 * Tmax);
-  if (warp == kProducer && lane == 0 && Tmax > 0) {
-    mbar_arrive_expect_tx(&bars.q_full, NQ * C::kQTile);
+  if (warp == kProducer) {
+    const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots);
+    if (lane == 0) {
+      item = pt;
+      if (pt.b >= 0) {
+        const OutWork<C> w(pt, slot, pair_heads, tile_rows);
+        if (w.Tmax > 0) {
+          mbar_arrive_expect_tx(&bars.q_full, NQ * C::kQTile);
 #pragma unroll
-    for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
-      load_tile<DH, kRows>(smem + g * C::kQTile, &maps.q, head[g], qr.first + (rows[g] ? row0[g] : row0[0]), &bars.q_full);
-    for (int x = 0; x < early; ++x) load_kv(x);
+          for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
+            load_tile<DH, kRows>(smem + g * C::kQTile, &maps.q, w.head[g], pt.q.first + (w.rows[g] ? w.row0[g] : w.row0[0]), &bars.q_full);
+          for (int x = 0; x < min(NST, 2 * w.Tmax); ++x) load_kv(x, pt.k.first);
+        }
+      }
+    }
+    __syncwarp();
   }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), wlim = p.wait_limit;
+  const PromptTile pt = item;
+  if (pt.b < 0) {   // no such tile
+    if (warp == kMma) tmem_dealloc(tmem, C::kTmem);
+    return;
+  }
+  const PackedRows qr = pt.q, kr = pt.k;
+  const int shift = kr.n - qr.n;
+  const OutWork<C> work(pt, slot, pair_heads, tile_rows);
+  const auto &head = work.head, &row0 = work.row0, &rows = work.rows, &T = work.T;
+  const int Tmax = work.Tmax, partial = work.partial, early = min(NST, 2 * Tmax);
   bool aborted = false;
 
   if (warp == kProducer) {
@@ -243,7 +264,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           aborted = true;
           break;
         }
-        if (lane == 0) load_kv(x);
+        if (lane == 0) load_kv(x, kr.first);
         ++issued;
       }
       if ((x & 1) && t == partial) {
@@ -413,10 +434,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float* w = v + 2 * j;
-            const float2 e0 = exp2_pair<0>(__ffma2_rn(make_float2(w[0], w[1]), cc, nb));
-            const float2 e1 = exp2_pair<1>(__ffma2_rn(make_float2(w[2], w[3]), cc, nb));
-            const float2 e2 = exp2_pair<2>(__ffma2_rn(make_float2(w[4], w[5]), cc, nb));
-            const float2 e3 = exp2_pair<3>(__ffma2_rn(make_float2(w[6], w[7]), cc, nb));
+            const float2 e0 = ex2_pair(__ffma2_rn(make_float2(w[0], w[1]), cc, nb));
+            const float2 e1 = ex2_pair(__ffma2_rn(make_float2(w[2], w[3]), cc, nb));
+            const float2 e2 = ex2_pair(__ffma2_rn(make_float2(w[4], w[5]), cc, nb));
+            const float2 e3 = ex2_pair(__ffma2_rn(make_float2(w[6], w[7]), cc, nb));
             s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
             s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
             u[j] = pack_bf16x2(e0.x, e0.y);
@@ -539,6 +560,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   __shared__ WeightBars<NST> bars;
   __shared__ float half_sum[kRows];
   __shared__ uint32_t tmem_base;
+  __shared__ PromptTile item;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const spatten_prompt_args& a = p.a;
@@ -569,28 +591,35 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
     *reinterpret_cast<uint4*>(smem + C::kTile + extra_at(tid, 1)) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
-  const PromptTile pt = find_prompt_tile<true>(a, kRows, blockIdx.x / a.H);
-  if (pt.b < 0) {   // no such tile
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    if (warp == kMma) tmem_dealloc(tmem_base, C::kTmem);
-    return;
-  }
+  grid_dep_trigger();
+  grid_dep_wait();
   const int h = blockIdx.x % a.H, G = a.H / a.H_kv, hk = h / G;
-  const PackedRows qr = pt.q, kr = pt.k;
-  const int j0 = pt.tile * kRows, shift = kr.n - qr.n;
-  const int rt0 = max(0, j0 - shift) / kRows;   // the first row tile that sees key j0
-  const int NT = max(0, (qr.n + kRows - 1) / kRows - rt0);
-
-  if (warp == kProducer && lane == 0 && NT > 0) {   // the keys, before the CTA meets
-    mbar_arrive_expect_tx(&bars.k_full, C::kTile);
-    load_tile<DH, kRows>(smem, &maps.k, hk, kr.first + j0, &bars.k_full);
+  auto first_tile = [](const PromptTile& pt) {   // of the row tiles that see the tile's first key
+    return max(0, pt.tile * kRows - (pt.k.n - pt.q.n)) / kRows;
+  };
+  if (warp == kProducer) {   // one warp looks the tile up and loads its keys before the CTA meets
+    const PromptTile pt = find_prompt_tile<true>(a, kRows, blockIdx.x / a.H);
+    if (lane == 0) {
+      item = pt;
+      if (pt.b >= 0 && (pt.q.n + kRows - 1) / kRows > first_tile(pt)) {
+        mbar_arrive_expect_tx(&bars.k_full, C::kTile);
+        load_tile<DH, kRows>(smem, &maps.k, hk, pt.k.first + pt.tile * kRows, &bars.k_full);
+      }
+    }
+    __syncwarp();
   }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), wlim = p.wait_limit;
+  const PromptTile pt = item;
+  if (pt.b < 0) {   // no such tile
+    if (warp == kMma) tmem_dealloc(tmem, C::kTmem);
+    return;
+  }
+  const PackedRows qr = pt.q, kr = pt.k;
+  const int j0 = pt.tile * kRows, shift = kr.n - qr.n;
+  const int rt0 = first_tile(pt), NT = max(0, (qr.n + kRows - 1) / kRows - rt0);
   bool aborted = false;
   float total = 0.0f;
 
@@ -685,10 +714,10 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
         if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
 #pragma unroll
         for (int q = 0; q < 64; q += 8) {
-          const float2 e0 = exp2_pair<0>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
-          const float2 e1 = exp2_pair<1>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
-          const float2 e2 = exp2_pair<2>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
-          const float2 e3 = exp2_pair<3>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
+          const float2 e0 = exp2_pair<0, kWeightPoly>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
+          const float2 e1 = exp2_pair<1, kWeightPoly>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
+          const float2 e2 = exp2_pair<2, kWeightPoly>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
+          const float2 e3 = exp2_pair<3, kWeightPoly>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
           s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
           s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
         }
@@ -736,6 +765,8 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
 
 // weight += the sums of a group's heads, in head order; blockIdx.y = key/value head
 __global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem p) {
+  grid_dep_trigger();
+  grid_dep_wait();
   const spatten_prompt_args& a = p.a;
   const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
   if (r >= a.total_kv) return;
@@ -807,14 +838,11 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
   const int64_t q_blocks = (static_cast<int64_t>(a.total_q) / tile_rows + a.B) * (pair_heads ? a.H / 2 : a.H);
   const int64_t k_blocks = (static_cast<int64_t>(a.total_kv) / kRows + a.B) * a.H;
   if (q_blocks > INT32_MAX || k_blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
-  prompt_out_kernel<O><<<static_cast<unsigned>(q_blocks), O::kThreads, O::kSmem, st>>>(p, maps);
-  SPT_TRY(launch_status());
+  SPT_TRY(launch_chained(prompt_out_kernel<O>, dim3(static_cast<unsigned>(q_blocks)), dim3(O::kThreads), O::kSmem, st, 1, p, maps));
   if (!a.weight) return SPATTEN_OK;
-  prompt_weight_kernel<W><<<static_cast<unsigned>(k_blocks), W::kThreads, W::kSmem, st>>>(p, maps);
-  SPT_TRY(launch_status());
+  SPT_TRY(launch_chained(prompt_weight_kernel<W>, dim3(static_cast<unsigned>(k_blocks)), dim3(W::kThreads), W::kSmem, st, 1, p, maps));
   if (a.H == a.H_kv) return SPATTEN_OK;
-  prompt_weight_reduce_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.total_kv, 256)), a.H_kv), 256, 0, st>>>(p);
-  return launch_status();
+  return launch_chained(prompt_weight_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(a.total_kv, 256)), a.H_kv), dim3(256), 0, st, 1, p);
 }
 
 }  // namespace

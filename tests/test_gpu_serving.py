@@ -622,3 +622,38 @@ def test_evict_more_rows_than_shared_memory_holds(cuda, in_place):
         src = R.evict_sources(w[b, 0], pos[b, 0], n[b], n[b], keep, recent)
         for k in before:
             np.testing.assert_array_equal(got[k][b, 0, :keep], before[k][b, 0, src], err_msg=k)
+
+
+def test_calls_back_to_back_see_each_other(cuda):
+    """A long run of dependent calls without a synchronisation: a kernel may start before the one ahead of it
+    has ended, but sees all that it wrote.  Appends, evictions, attention and reads of one state."""
+    S = lib()
+    B, H, d, cap, rows = 3, 2, 64, 96, 8
+    g = torch.Generator(device="cuda").manual_seed(77)
+    k, v = (torch.randn((40, B * rows, H, d), generator=g, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn((40, B, 4, d), generator=g, device="cuda").to(BF)
+
+    def run(sync):
+        c = Cache(S, B, H, d, cap, seed=3)
+        c.t["weight"].zero_()
+        ln, seen, status, cu = i32([0] * B), i32([0] * B), i32([0]), i32(offsets([rows] * B))
+        nb = S.kv4_evict_workspace_size(c.c, cap, 50)
+        w, out = ws(nb), []
+        for i in range(40):
+            S.kv4_append(c.c, k[i], v[i], H * d, B * rows, ln, ln, seen, seen, cu=cu, dev_status=status)
+            o = torch.empty_like(q[i])
+            a = S.make_kv4_attn_args(c.c, q[i], o, ln, cap, dev_status=status)
+            na = S.kv4_attention_workspace_size(a)
+            S.kv4_attention(a, ws(na), na)
+            ko, vo = (torch.empty((B * 50, H, d), dtype=BF, device="cuda") for _ in range(2))
+            S.kv4_evict(c.c, c.c, ln, ln, seen, cap, 50, 5, w, nb, status)
+            S.kv4_read(c.c, i32(offsets([50] * B)), B * 50, ko, vo, H * d, dev_status=status)
+            out += [o, ko, vo]
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return out + list(c.t.values()) + [ln, seen]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
