@@ -140,76 +140,85 @@ struct Warp {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kQ = kF32 ? 2 : 1;   // terms of a query
   static constexpr int kP = kF32 ? 3 : 1;   // terms of a P'
-  // what the lanes need of one column of heads, made once per CTA
+  // what the lanes need of one column of heads, made once per CTA, a warp for each group of channels
   struct Query {
     uint4 q[kQ][G32][32];         // B operand of the scores: (step, half) of a group
-    uint2 start[32];              // B operand of the scores' start
-    float2 scale[32];             // factor to log2 units
+    float sum[8][G32];            // -8 2^-24 sum(q) of each head's groups
+    float scale[8];               // factor to log2 units
   };
+  static constexpr int kPrepareWarps = NH * G32;
   uint32_t q[NH][kQ][G32][4];
   uint32_t start[NH][2];
   float scale[NH][2];
   float o[NH][DH / 16][4];
   float lim[NH][2], nb[NH][2], l[NH][2];    // maximum + kRescale, what the exponents add (-maximum, or 0), sum of this lane's keys
 
-  // column nh: heads h0 + 8 nh .. of query row qrow (heads past `heads` are zeros); one warp
-  static __device__ __forceinline__ void prepare(Query& out, const T* qrow, int nh, int heads, float sm_scale, int lane) {
-    const int gid = lane >> 2, t = lane & 3, h = nh * 8 + gid;
-    float f[G32][8], start[G32], amax = 0.0f;
+  // a lane's share of a head's channels: of every group eight, as they are loaded
+  struct Raw {
+    uint4 u[G32][sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* qrow, int nh, int heads, int lane) {   // heads past `heads` are zeros
+      const int h = nh * 8 + (lane >> 2);
+#pragma unroll
+      for (int j = 0; j < G32; ++j)
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+          u[j][i] = h < heads ? reinterpret_cast<const uint4*>(qrow + static_cast<int64_t>(h) * DH + 32 * j + 8 * (lane & 3))[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(int j, float* x) const {
+      const uint32_t w[4] = {u[j][0].x, u[j][0].y, u[j][0].z, u[j][0].w};
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf_lo(w[i]), x[2 * i + 1] = bf_hi(w[i]);
+      } else {
+        const uint4 v = u[j][sizeof(T) / 2 - 1];
+        const uint32_t w1[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]), x[4 + i] = __uint_as_float(w1[i]);
+      }
+    }
+  };
+  // group `own` of a column of heads; one warp
+  static __device__ __forceinline__ void prepare(Query& out, const Raw& raw, int own, float sm_scale, int lane) {
+    const int gid = lane >> 2, t = lane & 3;
+    float g[8], amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < G32; ++j) {
+      float x[8];
+      raw.get(j, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
-      if (h < heads) load8(qrow + static_cast<int64_t>(h) * DH + 32 * j + 8 * t, f[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[j][i]));
+      for (int i = 0; i < 8; ++i) {
+        amax = fmaxf(amax, fabsf(x[i]));
+        g[i] = j == 0 || j == own ? x[i] : g[i];
+      }
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     // 2^E q has its maximum in [2^13, 2^14); E stays where 2^E and 2^(12 - E) are normal numbers
     const int E = max(-114, min(126, 13 + 127 - static_cast<int>(__float_as_uint(amax) >> 23)));
     const float up = __uint_as_float(static_cast<uint32_t>(E + 127) << 23);
-    const float sc = sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(12 - E + 127) << 23);
+    float sum = 0.0f;
+    uint32_t u[kQ][4];
 #pragma unroll
-    for (int j = 0; j < G32; ++j) {
-      float sum = 0.0f;
-      uint32_t u[kQ][4];
+    for (int c = 0; c < 4; ++c) {   // channels c, c + 4 of the word; the odd ones against 16 u
+      const float w = (c & 1) ? 0.0625f : 1.0f;
+      float x = g[c] * up * w, y = g[c + 4] * up * w;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {   // channels c, c + 4 of the word; the odd ones against 16 u
-        const float w = (c & 1) ? 0.0625f : 1.0f;
-        float x = f[j][c] * up * w, y = f[j][c + 4] * up * w;
-#pragma unroll
-        for (int e = 0; e < kQ; ++e) {
-          u[e][c] = pack_half(x, y);
-          const float2 r = half_pair(u[e][c]);
-          sum += (r.x + r.y) * ((c & 1) ? 16.0f : 1.0f);
-          x -= r.x;
-          y -= r.y;
-        }
+      for (int e = 0; e < kQ; ++e) {
+        u[e][c] = pack_half(x, y);
+        const float2 r = half_pair(u[e][c]);
+        sum += (r.x + r.y) * ((c & 1) ? 16.0f : 1.0f);
+        x -= r.x;
+        y -= r.y;
       }
-#pragma unroll
-      for (int e = 0; e < kQ; ++e) out.q[e][j][lane] = make_uint4(u[e][0], u[e][1], u[e][2], u[e][3]);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      start[j] = sum * (-8.0f * 5.9604644775390625e-08f);   // -8 2^-24
     }
-    // -8 sum(q) of the groups as three bfloat16 each, along the operand's 16 rows against the keys' scales:
-    // rows 2t, 2t + 1 hold a term of two groups (128 channels: t = 0, 1 the first, 2, 3 the second, 0, 1 of
-    // the upper eight the third; 64: t = 0, 1, 2)
-    uint32_t term[3][G32 / 2];
 #pragma unroll
-    for (int e = 0; e < 3; ++e)
-#pragma unroll
-      for (int j = 0; j < G32 / 2; ++j) {
-        term[e][j] = pack_bf16(start[2 * j], start[2 * j + 1]);
-        start[2 * j] -= bf_lo(term[e][j]);
-        start[2 * j + 1] -= bf_hi(term[e][j]);
-      }
-    if constexpr (DH == 128)
-      out.start[lane] = make_uint2((t & 1) ? term[t >> 1][1] : term[t >> 1][0], t > 1 ? 0u : term[2][t & 1]);
-    else
-      out.start[lane] = make_uint2(t == 3 ? 0u : term[t][0], 0u);
-    out.scale[lane] = make_float2(__shfl_sync(0xffffffffu, sc, 8 * t), __shfl_sync(0xffffffffu, sc, 8 * t + 4));
+    for (int e = 0; e < kQ; ++e) out.q[e][own][lane] = make_uint4(u[e][0], u[e][1], u[e][2], u[e][3]);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (t == 0) {
+      out.sum[gid][own] = sum * (-8.0f * 5.9604644775390625e-08f);   // -8 2^-24
+      if (own == 0) out.scale[gid] = sm_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(12 - E + 127) << 23);
+    }
   }
 
   __device__ __forceinline__ void init(const Query* in, int lane) {
@@ -223,9 +232,22 @@ struct Warp {
           q[nh][e][j][0] = u.x, q[nh][e][j][1] = u.y, q[nh][e][j][2] = u.z, q[nh][e][j][3] = u.w;
         }
       }
-      const uint2 st = in[nh].start[lane];
-      start[nh][0] = st.x, start[nh][1] = st.y;
-      const float2 sc = in[nh].scale[lane];
+      // -8 sum(q) of the groups as three bfloat16 each, along the operand's 16 rows against the keys' scales:
+      // rows 2t, 2t + 1 hold a term of two groups (128 channels: t = 0, 1 the first, 2, 3 the second, 0, 1 of
+      // the upper eight the third; 64: t = 0, 1, 2)
+      const int t = lane & 3;
+      const float2 st = *reinterpret_cast<const float2*>(&in[nh].sum[lane >> 2][DH == 128 ? 2 * (t & 1) : 0]);
+      const uint32_t t0 = pack_bf16(st.x, st.y);
+      const float x1 = st.x - bf_lo(t0), y1 = st.y - bf_hi(t0);
+      const uint32_t t1 = pack_bf16(x1, y1), t2 = pack_bf16(x1 - bf_lo(t1), y1 - bf_hi(t1));
+      if constexpr (DH == 128) {
+        start[nh][0] = t < 2 ? t0 : t1;
+        start[nh][1] = t < 2 ? t2 : 0u;
+      } else {
+        start[nh][0] = t == 0 ? t0 : (t == 1 ? t1 : (t == 2 ? t2 : 0u));
+        start[nh][1] = 0u;
+      }
+      const float2 sc = *reinterpret_cast<const float2*>(&in[nh].scale[2 * t]);
       scale[nh][0] = sc.x, scale[nh][1] = sc.y;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -391,6 +413,7 @@ template <int DH, int NH, typename T>
 __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) kv4_attn_kernel(AttnArgs args) {
   using W = Warp<DH, NH, T>;
   constexpr int TK = W::TK, G32 = W::G32, kHeads = NH * 8;
+  constexpr int kPart = ring_bytes(DH, NH) / kWarps / 4;   // floats of a warp's share of the rings
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings (later their sums), then the scores
   __shared__ __align__(16) typename W::Query query[NH];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
@@ -398,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   __shared__ float2 in_ml[kMaxC][kHeads];
   __shared__ float in_o[kHeads * DH];
   __shared__ float2 f[kHeads];                   // the cluster's maxima, and sums inverted
+  __shared__ float rank_factor[kMaxC][kHeads];
   grid_dep_trigger();
   grid_dep_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -407,6 +431,10 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   const int hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, t = lane & 3;
   const int group = a.H / c.H_kv;
+  // the query's loads go out first: what follows them waits for the length
+  typename W::Raw raw;
+  const T* qrow = static_cast<const T*>(a.q) + b * a.q_ld + static_cast<int64_t>(hk) * group * DH;
+  if (warp < W::kPrepareWarps) raw.load(qrow, warp / G32, min(kHeads, group), lane);
   const int n_all = clamp_len(a.len[b], a.n_max, a.dev_status);
   const int run = (((n_all + C - 1) / C) + TK - 1) / TK * TK;   // keys per CTA
   const int first = min(n_all, rank * run), n = min(run, n_all - first);
@@ -470,9 +498,10 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
       if (warp + kWarps * i < tiles) load(i, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    if (warp < NH)
-      W::prepare(query[warp], static_cast<const T*>(a.q) + b * a.q_ld + (static_cast<int64_t>(hk) * group + h0) * DH, warp, heads,
-                 a.sm_scale, lane);
+    if (warp < W::kPrepareWarps) {
+      if (h0) raw.load(qrow + static_cast<int64_t>(h0) * DH, warp / G32, heads, lane);
+      W::prepare(query[warp / G32], raw, warp % G32, a.sm_scale, lane);
+    }
     __syncthreads();
     W w;
     w.init(query, lane);
@@ -511,42 +540,47 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
           s_l[warp][nh * 8 + 2 * t + k] = l;
         }
       }
-    __syncthreads();   // also: every ring is free, and the query has been read
-    float* part = reinterpret_cast<float*>(smem);   // [warp][head][channel]
+    __syncwarp();
+    float* part = reinterpret_cast<float*>(smem);   // [warp][head][channel]: over the warp's own ring (and, 16 heads, more)
+    if (ring_bytes(DH, NH) > kWarps * kStages * kStageBytes) __syncthreads();   // which others may still read
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int h = nh * 8 + 2 * t + k;
         if (h < heads) {
-          float mx = s_m[0][h];
-#pragma unroll
-          for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][h]);
-          const float scale = ex2(w.maximum(nh, k) - (mx == -INFINITY ? 0.0f : mx));
-          float* dst = part + (warp * kHeads + h) * DH + 4 * gid;
+          float* dst = part + warp * kPart + h * DH + 4 * gid;
 #pragma unroll
           for (int j = 0; j < G32; ++j)   // channels 32 j + 4 gid .. + 3
-            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(w.o[nh][2 * j][k] * scale, w.o[nh][2 * j][k + 2] * scale,
-                                                                   w.o[nh][2 * j + 1][k] * scale, w.o[nh][2 * j + 1][k + 2] * scale);
+            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(w.o[nh][2 * j][k], w.o[nh][2 * j][k + 2], w.o[nh][2 * j + 1][k], w.o[nh][2 * j + 1][k + 2]);
         }
       }
-    if (C > 1 && h0 == 0) cluster.barrier_wait();   // every CTA does
-    if (tid < heads * C) {   // the CTA's maxima and sums to every CTA
+    if (C > 1 && h0 == 0) cluster.barrier_wait();   // every CTA of the cluster runs
+    __syncthreads();
+    // the maximum of a head over the CTA's warps, and the factors of their sums
+    auto warp_factors = [&](int h, float* fac) {
+      float m[kWarps], mx = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) mx = fmaxf(mx, m[v] = s_m[v][h]);
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) fac[v] = ex2(m[v] - (mx == -INFINITY ? 0.0f : mx));
+      return mx;
+    };
+    float fac[kWarps];
+    if (tid < heads * C) {   // maxima and sums to every CTA
       const int h = tid % heads;
-      float mx = s_m[0][h], l = 0.0f;
+      const float mx = warp_factors(h, fac);
+      float l = 0.0f;
 #pragma unroll
-      for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][h]);
-      const float base = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][h], ex2(s_m[v][h] - base), l);
+      for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][h], fac[v], l);
       *cluster.map_shared_rank(&in_ml[rank][h], tid / heads) = make_float2(mx, l);
     }
-    __syncthreads();
     const int share = heads * DH / C;   // the outputs that a CTA adds up
     for (int e = tid; e < heads * DH; e += kThreads) {
+      warp_factors(e / DH, fac);
       float v = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += part[k * kHeads * DH + e];
+      for (int k = 0; k < kWarps; ++k) v = fmaf(part[k * kPart + e], fac[k], v);
       const int to = e / share;
       *cluster.map_shared_rank(&in_o[rank * share + (e - to * share)], to) = v;
     }
@@ -554,17 +588,28 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
     else __syncthreads();
     // the cluster's sums, in rank order
     if (tid < heads) {
+      float2 ml[kMaxC];
       float mx = -INFINITY, l = 0.0f;
-      for (int r = 0; r < C; ++r) mx = fmaxf(mx, in_ml[r][tid].x);
+#pragma unroll
+      for (int r = 0; r < kMaxC; ++r) ml[r] = r < C ? in_ml[r][tid] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int r = 0; r < kMaxC; ++r) mx = fmaxf(mx, ml[r].x);
       const float base = mx == -INFINITY ? 0.0f : mx;
-      for (int r = 0; r < C; ++r) l = fmaf(in_ml[r][tid].y, ex2(in_ml[r][tid].x - base), l);
+#pragma unroll
+      for (int r = 0; r < kMaxC; ++r) {
+        const float g = ex2(ml[r].x - base);
+        l = fmaf(ml[r].y, g, l);
+        rank_factor[r][tid] = g;
+      }
       f[tid] = make_float2(base, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));   // an empty sequence gives 0, NaN stays
     }
     __syncthreads();
     for (int e = tid; e < share; e += kThreads) {
       const int h = (rank * share + e) / DH;
       float v = 0.0f;
-      for (int r = 0; r < C; ++r) v = fmaf(in_o[r * share + e], ex2(in_ml[r][h].x - f[h].x), v);
+#pragma unroll
+      for (int r = 0; r < kMaxC; ++r)
+        if (r < C) v = fmaf(in_o[r * share + e], rank_factor[r][h], v);
       st_from_float(static_cast<T*>(a.o) + b * a.o_ld + (static_cast<int64_t>(hk) * group + h0) * DH + rank * share + e, v * f[h].y);
     }
     if (x) {

@@ -1,4 +1,5 @@
 // spatten_prompt_attention: argument checks, workspace and kernel choice.
+#include <algorithm>
 #include <cmath>
 
 #include "attention.cuh"
@@ -6,6 +7,9 @@
 
 namespace spt {
 namespace {
+
+// A poll may block for some microseconds, so this many are a few seconds.
+constexpr uint32_t kPromptWaitLimit = 1u << 20;
 
 int32_t validate(const spatten_prompt_args& a) {
   if (a.B < 1 || a.B > 65535 || a.H < 1 || a.H > 1024 || a.H_kv < 1) return SPATTEN_E_ARG;
@@ -33,25 +37,58 @@ int32_t validate(const spatten_prompt_args& a) {
 bool use_tc(const spatten_prompt_args& a) { return a.kernel != SPATTEN_ATTN_CUDA_CORE && prompt_tc_supported(a); }
 
 size_t layout(const spatten_prompt_args& a, void* ws, size_t ws_bytes, PromptProblem* p) {
-  if (!a.weight) return 0;
+  const bool tc = use_tc(a);
+  const bool split = tc && a.dtype == SPATTEN_F32 && a.total_q > 0;
+  if (!a.weight && !split) return 0;
   WsCursor c(ws, ws_bytes);
-  const size_t rows = static_cast<size_t>(a.H) * a.total_q;
-  if (use_tc(a)) {
-    float* offset = c.take<float>(rows);
-    float* part = a.H > a.H_kv ? c.take<float>(static_cast<size_t>(a.H) * a.total_kv) : nullptr;
-    if (p) p->offset = offset, p->part = part;
-  } else {
-    float2* stats = c.take<float2>(rows);
-    if (p) p->stats = stats;
+  uint16_t* planes[3] = {};
+  if (split)
+    for (int t = 0; t < 3; ++t)
+      planes[t] = c.take<uint16_t>(3 * static_cast<size_t>(t == 0 ? a.total_q : a.total_kv) * (t == 0 ? a.H : a.H_kv) * a.d_h);
+  const size_t rows = a.weight ? static_cast<size_t>(a.H) * a.total_q : 0;
+  float* offset = a.weight && tc ? c.take<float>(rows) : nullptr;
+  float2* stats = a.weight && !tc ? c.take<float2>(rows) : nullptr;
+  float* part = a.weight && a.H > a.H_kv ? c.take<float>(static_cast<size_t>(a.H) * a.total_kv) : nullptr;
+  if (p) {
+    for (int t = 0; t < 3; ++t) p->planes[t] = planes[t];
+    p->offset = offset, p->stats = stats, p->part = part;
   }
   return align_up(c.used, 256);
 }
 
+// weight += the sums of a group's heads, in head order; blockIdx.y = key/value head
+__global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem p) {
+  grid_dep_trigger();
+  grid_dep_wait();
+  const spatten_prompt_args& a = p.a;
+  const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
+  if (r >= a.total_kv) return;
+  const int b = owner_of_row(a.cu_kv, a.B, r);
+  if (b < 0) return;
+  const PackedRows kr = packed_rows(a.cu_kv, b, a.total_kv);
+  const int j = r - kr.first;
+  if (kr.bad || j < 0 || j >= kr.n) return;
+  if (j >= a.weight_cap) {
+    report(a.dev_status, SPATTEN_E_INDEX);
+    return;
+  }
+  const float* part = p.part + static_cast<int64_t>(hk) * G * a.total_kv + r;
+  float sum = 0.0f;
+  for (int g = 0; g < G; ++g) sum += part[static_cast<int64_t>(g) * a.total_kv];
+  a.weight[static_cast<int64_t>(b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
+}
+
 }  // namespace
+
+int32_t prompt_reduce_launch(const PromptProblem& p, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.a.total_kv, 256)), p.a.H_kv);
+  return launch_chained(prompt_weight_reduce_kernel, grid, dim3(256), 0, st, 1, p);
+}
+
 }  // namespace spt
 
 extern "C" size_t spatten_prompt_workspace_size(const spatten_prompt_args* a) {
-  if (!a || a->H < 1 || a->total_q < 0 || a->total_kv < 0) return 0;
+  if (!a || a->H < 1 || a->H_kv < 1 || a->d_h < 1 || a->total_q < 0 || a->total_kv < 0) return 0;
   return spt::layout(*a, nullptr, 0, nullptr);
 }
 
@@ -62,7 +99,7 @@ extern "C" int32_t spatten_prompt_attention(const spatten_prompt_args* a, void* 
   SPT_TRY(validate(*a));
   PromptProblem p{};
   p.a = *a;
-  p.wait_limit = wait_limit_setting();
+  p.wait_limit = std::min(wait_limit_setting(), kPromptWaitLimit);
   const size_t need = layout(*a, ws, ws_bytes, &p);
   if (need && (!ws || ws_bytes < need)) return SPATTEN_E_WORKSPACE;
   if (need && !aligned16(ws)) return SPATTEN_E_ALIGN;

@@ -7,12 +7,14 @@ namespace spt {
 
 struct PromptProblem {
   spatten_prompt_args a;   // sm_scale > 0 and cu_kv set
-  // with weights only (else NULL).  CUDA cores: [H][total_q] score maximum (log2 units) and exponential
-  // sum of each row.  Tensor cores: [H][total_q] what each row's scores need added (before the softmax
-  // scale) for their exponentials to be P, and [H][total_kv] the heads' column sums (grouped heads).
+  // with weights only (else NULL)
+  // [H][total_q] CUDA cores: score maximum (log2 units) and reciprocal of the exponential sum of each row
+  // (0, 0 where a row sees nothing); tensor cores: what each row's scores need added (before the softmax
+  // scale) for their exponentials to be P
   float2* stats;
   float* offset;
-  float* part;
+  uint16_t* planes[3];     // float32 on tensor cores: q, k, v as [3][rows][heads][d_h] bfloat16 terms
+  float* part;             // [H][total_kv] the heads' column sums (grouped heads)
   uint32_t wait_limit;     // polls of one pipeline wait (tensor-core kernels)
 };
 
@@ -86,6 +88,7 @@ __device__ __forceinline__ void report_bad_offsets(const spatten_prompt_args& a)
 }
 
 int32_t prompt_simt_launch(const PromptProblem& p, cudaStream_t st);
+int32_t prompt_reduce_launch(const PromptProblem& p, cudaStream_t st);   // weight += the heads' column sums
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st);
 bool prompt_tc_supported(const spatten_prompt_args& a);
 

@@ -1,4 +1,6 @@
-// Prompt attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), bfloat16.
+// Prompt attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), bfloat16; float32 operands as
+// sums of three bfloat16 planes, which a first kernel splits them into, and six products of planes (24 bits;
+// on CUDA cores the multiply-adds took <F32_SIMT>).
 //
 // Two kernels, and a small third one when several query heads share a key/value head:
 //  OUTPUT  one pass over the visible keys in tiles of 128 with the running maximum and sum of the
@@ -10,7 +12,7 @@
 //  WEIGHT  weight_j = sum_i exp(S_ij - m_i) / l_i needs final statistics, hence a second pass over the
 //          scores, transposed: S^T = K Q^T puts one key on each TMEM lane, so the sum over the rows stays
 //          inside a thread (no exchange between lanes) and runs in a fixed order.
-//  REDUCE  the heads of a group add up in head order.
+//  The heads of a group add up in a third, small one.
 // What bounds them: exponentials (16 per clock and SM; a quarter of the unmasked ones goes to the FMA
 // pipe, exp2_poly.cuh) next to the tensor cores; O's rescaling is skipped while no row's maximum has
 // grown by more than 2^8, which float32 sums and the bfloat16 P bear without loss (P is relative).
@@ -18,7 +20,9 @@
 // copies and MMAs, frees its TMEM and returns.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "exp2_poly.cuh"
@@ -34,6 +38,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;             // rows of a query tile (and, for the weights, keys of a key tile)
 constexpr int kBox = 64;               // rows of a TMA box
 constexpr float kRescale = 8.0f;       // growth of a row's maximum (log2) that makes O be rescaled
+
+// The three planes of a pair of float32: each takes the high half of what is left, cut off (a sum of 24 bits).
+__device__ __forceinline__ uint32_t split_pair(float2 x, uint32_t& mid, uint32_t& low) {
+  const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+  const float r0 = x.x - __uint_as_float(a & 0xffff0000u), r1 = x.y - __uint_as_float(b & 0xffff0000u);
+  const uint32_t c = __float_as_uint(r0), d = __float_as_uint(r1);
+  mid = __byte_perm(c, d, 0x7632);
+  low = __byte_perm(__float_as_uint(r0 - __uint_as_float(c & 0xffff0000u)), __float_as_uint(r1 - __uint_as_float(d & 0xffff0000u)), 0x7632);
+  return __byte_perm(a, b, 0x7632);
+}
 
 __device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 // the same by the FMA pipe for the first POLY of every four pairs (Q: the pair)
@@ -71,13 +85,29 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// all of a [ROWS x DH] tile: blocks of 64 channels, each the rows' 128 bytes one behind the other
-template <int DH, int ROWS>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, uint64_t* bar) {
+// All of a [ROWS x DH] tile: blocks of 64 channels, each the rows' 128 bytes one behind the other; of PL planes,
+// whose rows are `plane` rows apart, one tile behind the other.
+template <int DH, int ROWS, int PL>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, int plane, uint64_t* bar) {
 #pragma unroll
-  for (int c = 0; c < DH / 64; ++c)
+  for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-    for (int r = 0; r < ROWS; r += kBox) tma_load_3d(dst + (c * ROWS + r) * 128, map, c * 64, head, row + r, bar);
+    for (int c = 0; c < DH / 64; ++c)
+#pragma unroll
+      for (int r = 0; r < ROWS; r += kBox)
+        tma_load_3d(dst + ((pl * (DH / 64) + c) * ROWS + r) * 128, map, c * 64, head, pl * plane + row + r, bar);
+}
+
+// Float32 operands are sums of three bfloat16 planes (24 bits); of their nine products those within 2^-24 of the
+// largest are made, small ones first.
+template <int PL> constexpr int kProducts = PL == 1 ? 1 : 6;
+template <int PL>
+__device__ __forceinline__ constexpr int product_a(int i) {
+  return PL == 1 ? 0 : (i == 0 ? 2 : (i == 2 || i == 3 ? 1 : 0));
+}
+template <int PL>
+__device__ __forceinline__ constexpr int product_b(int i) {
+  return PL == 1 ? 0 : (i == 1 ? 2 : (i == 2 || i == 4 ? 1 : 0));
 }
 
 // The MMA warp runs its loop as a whole and elects a lane (the same one every time) for the instructions
@@ -105,22 +135,33 @@ template <int ROWS>
 __device__ __forceinline__ uint64_t desc_cols(uint32_t saddr) { return desc_sw128(saddr, ROWS * 128u, 1024); }    // MN-major
 
 // D[128 x N] = A B^T over DH channels, both tiles K-major
-template <int DH, int N>
+template <int DH, int N, int PL>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b) {
   constexpr uint32_t id = idesc_bf16(128, N, false, false);
 #pragma unroll
-  for (int s = 0; s < DH / 16; ++s) {
-    const uint32_t at = ((s >> 2) * (kRows * 128u) + (s & 3) * 32u) >> 4, bt = ((s >> 2) * (N * 128u) + (s & 3) * 32u) >> 4;
-    if (elect_one()) mma_f16(d, a + at, b + bt, id, s > 0 ? 1u : 0u);
-  }
+  for (int i = 0; i < kProducts<PL>; ++i)
+#pragma unroll
+    for (int s = 0; s < DH / 16; ++s) {
+      const uint32_t at = (product_a<PL>(i) * (kRows * DH * 2u) + (s >> 2) * (kRows * 128u) + (s & 3) * 32u) >> 4;
+      const uint32_t bt = (product_b<PL>(i) * (N * DH * 2u) + (s >> 2) * (N * 128u) + (s & 3) * 32u) >> 4;
+      if (elect_one()) mma_f16(d, a + at, b + bt, id, i > 0 || s > 0 ? 1u : 0u);
+    }
 }
-// O (+)= P V: P in TMEM (8 columns per 16 keys, the second 64 keys 64 columns on), V rows MN-major
-template <int DH, int KT>
+// O (+)= P V: P in TMEM (8 columns per 16 keys, the second 64 keys 64 columns on; further planes of P behind
+// the KT columns of the scores, 32 each: KT is 64 then), V rows MN-major
+template <int DH, int KT, int PL>
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t acc) {
   constexpr uint32_t id = idesc_bf16(128, DH, false, true);
+  static_assert(PL == 1 || KT == 64, "planes of P");
 #pragma unroll
-  for (int s = 0; s < KT / 16; ++s)
-    if (elect_one()) mma_f16_ts(d, p + (s & 3) * 8 + (s >> 2) * 64, v + s * (2048u >> 4), id, (acc || s > 0) ? 1u : 0u);
+  for (int i = 0; i < kProducts<PL>; ++i) {
+    const int pa = product_a<PL>(i);
+#pragma unroll
+    for (int s = 0; s < KT / 16; ++s)
+      if (elect_one())
+        mma_f16_ts(d, p + (pa ? KT + (pa - 1) * 32 : 0) + (s & 3) * 8 + (s >> 2) * 64,
+                   v + ((product_b<PL>(i) * (KT * DH * 2u) + s * 2048u) >> 4), id, (acc || i > 0 || s > 0) ? 1u : 0u);
+  }
 }
 
 struct Maps {
@@ -132,18 +173,19 @@ struct Maps {
 // =================================================================================================
 // NQ query tiles a CTA, tiles of KT keys.  One thread has a row and 64 keys of each tile; where a tile has 128
 // keys the two threads of a row share its maximum.
-template <int DH_, int NQ_, int KT_, int STAGES>
+template <int DH_, int NQ_, int KT_, int STAGES, int PL_ = 1>
 struct OutCfg {
-  static constexpr int DH = DH_, NQ = NQ_, KT = KT_, kHalves = KT / 64;
+  static constexpr int DH = DH_, NQ = NQ_, KT = KT_, PL = PL_, kHalves = KT / 64;
   static constexpr int kStages = STAGES;                 // K and V tiles in flight, one ring
-  static constexpr uint32_t kQTile = kRows * DH * 2u, kTile = KT * DH * 2u;
+  static constexpr uint32_t kQTile = PL * kRows * DH * 2u, kTile = PL * KT * DH * 2u;
   static constexpr uint32_t oKV = NQ * kQTile;
   static constexpr uint32_t kSmem = oKV + kStages * kTile + 1024u;
   static constexpr int kGroup = 128 * kHalves;           // softmax threads of a query tile
   static constexpr int kThreads = NQ * kGroup + 64;
-  static constexpr uint32_t kColumns = NQ * (KT + DH), kTmem = kColumns <= 128 ? 128 : (kColumns <= 256 ? 256 : 512);
-  static constexpr int kCtas = 512 / kTmem;              // per SM
-  static constexpr uint32_t tS = 0, tO = NQ * KT;
+  static constexpr uint32_t kScores = KT + (PL - 1) * 32;   // columns of a tile's scores and further planes of P
+  static constexpr uint32_t kColumns = NQ * (kScores + DH), kTmem = kColumns <= 128 ? 128 : (kColumns <= 256 ? 256 : 512);
+  static constexpr int kCtas = 2 * kSmem > 226 * 1024 ? 1 : 512 / kTmem;   // per SM
+  static constexpr uint32_t tS = 0, tO = NQ * kScores;
 };
 
 template <int NQ, int NST>
@@ -173,7 +215,7 @@ struct OutWork {
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
-  constexpr int DH = C::DH, NQ = C::NQ, KT = C::KT, NST = C::kStages, kHalves = C::kHalves;
+  constexpr int DH = C::DH, NQ = C::NQ, KT = C::KT, PL = C::PL, NST = C::kStages, kHalves = C::kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ OutBars<NQ, NST> bars;
@@ -219,7 +261,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
   auto load_kv = [&](int x, int first) {   // the ring's x-th tile: K0 V0 K1 V1 ..
     mbar_arrive_expect_tx(&bars.kv_full[x % NST], C::kTile);
-    load_tile<DH, KT>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, first + (x >> 1) * KT, &bars.kv_full[x % NST]);
+    load_tile<DH, KT, PL>(smem + C::oKV + (x % NST) * C::kTile, (x & 1) ? &maps.v : &maps.k, hk, first + (x >> 1) * KT, a.total_kv,
+                          &bars.kv_full[x % NST]);
   };
   if (warp == kProducer) {
     const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots);
@@ -231,7 +274,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           mbar_arrive_expect_tx(&bars.q_full, NQ * C::kQTile);
 #pragma unroll
           for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
-            load_tile<DH, kRows>(smem + g * C::kQTile, &maps.q, w.head[g], pt.q.first + (w.rows[g] ? w.row0[g] : w.row0[0]), &bars.q_full);
+            load_tile<DH, kRows, PL>(smem + g * C::kQTile, &maps.q, w.head[g], pt.q.first + (w.rows[g] ? w.row0[g] : w.row0[0]), a.total_q,
+                                     &bars.q_full);
           for (int x = 0; x < min(NST, 2 * w.Tmax); ++x) load_kv(x, pt.k.first);
         }
       }
@@ -277,7 +321,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         const int first = kr.n - t * KT;
         for (int e = first * 8 + lane; e < KT * 8; e += 32)
 #pragma unroll
-          for (int c = 0; c < DH / 64; ++c)
+          for (int c = 0; c < PL * DH / 64; ++c)
             *reinterpret_cast<uint4*>(dst + c * KT * 128 + sw128_offset(e >> 3, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
         mbar_arrive(&bars.v_fix);
@@ -300,7 +344,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
 #pragma unroll
         for (int g = 0; g < NQ; ++g)
           if (T[g] > 0) {
-            mma_scores<DH, KT>(tmem + C::tS + g * KT, dQ + g * (C::kQTile >> 4), dK);
+            mma_scores<DH, KT, PL>(tmem + C::tS + g * C::kScores, dQ + g * (C::kQTile >> 4), dK);
             commit_one(&bars.s_full[g]);
           }
         commit_one(&bars.kv_empty[0]);
@@ -308,7 +352,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       // One tile's P V and next scores run while the other tile's softmax does.  Between two tiles' MMAs there
       // is only the wait for P: the tensor cores idle meanwhile.  (An MMA warp per tile was slower, 675 us
       // against 519: the tiles' MMAs then alternate in the pipe.)
-      int sv = 1, sk = 2 % NST, pv = 0, pk = 0;   // the ring's stages of V(t) and K(t + 1), and their phases
+      int sv = 1, sk = 2 % NST, pv = 0, pk = (2 / NST) & 1;   // the ring's stages of V(t) and K(t + 1), and their phases
       for (int t = 0; t < Tmax && !aborted; ++t) {
         const bool more = t + 1 < Tmax;
         if (!wait(&bars.kv_full[sv], pv) || (t == partial && !wait(&bars.v_fix, 0)) || (more && !wait(&bars.kv_full[sk], pk))) break;
@@ -318,9 +362,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           if (t >= T[g]) continue;
           if (!wait(&bars.p_ready[g], t & 1)) break;
           tc_after_sync();
-          mma_pv<DH, KT>(tmem + C::tO + g * DH, tmem + C::tS + g * KT, dVt, t > 0 ? 1u : 0u);
+          mma_pv<DH, KT, PL>(tmem + C::tO + g * DH, tmem + C::tS + g * C::kScores, dVt, t > 0 ? 1u : 0u);
           if (t + 1 < T[g]) {
-            mma_scores<DH, KT>(tmem + C::tS + g * KT, dQ + g * (C::kQTile >> 4), dKt);   // over the P that the MMAs before it read
+            mma_scores<DH, KT, PL>(tmem + C::tS + g * C::kScores, dQ + g * (C::kQTile >> 4), dKt);   // over the P that the MMAs before it read
             commit_one(&bars.s_full[g]);
           } else {
             commit_one(&bars.o_full[g]);
@@ -345,7 +389,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     const int my_head = g ? head[NQ - 1] : head[0];
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's TMEM lanes (32 (warp & 3)) << 16
     constexpr int kOCols = DH / kHalves;                            // columns of O that this thread scales and stores
-    const uint32_t tS = tmem + lanes + C::tS + g * KT + half * 64, tO = tmem + lanes + C::tO + g * DH + half * kOCols;
+    const uint32_t tS = tmem + lanes + C::tS + g * C::kScores + half * 64, tO = tmem + lanes + C::tO + g * DH + half * kOCols;
     // the last key that this row sees, and that the warp's first one does
     const int last = min(my_row0 + r + shift, kr.n - 1), warp_row = my_row0 + (warp & 3) * 32;
     const int last_first = min(warp_row + shift, kr.n - 1), last_last = min(warp_row + 31 + shift, kr.n - 1);
@@ -427,7 +471,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       if (full) {
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          uint32_t u[16];
+          uint32_t u[16], u2[PL == 3 ? 16 : 1], u3[PL == 3 ? 16 : 1];
           float v[32];
           tmem_ld32(tS + ch * 32, v);
           tmem_ld_wait();
@@ -440,17 +484,28 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
             const float2 e3 = ex2_pair(__ffma2_rn(make_float2(w[6], w[7]), cc, nb));
             s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
             s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
-            u[j] = pack_bf16x2(e0.x, e0.y);
-            u[j + 1] = pack_bf16x2(e1.x, e1.y);
-            u[j + 2] = pack_bf16x2(e2.x, e2.y);
-            u[j + 3] = pack_bf16x2(e3.x, e3.y);
+            if constexpr (PL == 1) {
+              u[j] = pack_bf16x2(e0.x, e0.y);
+              u[j + 1] = pack_bf16x2(e1.x, e1.y);
+              u[j + 2] = pack_bf16x2(e2.x, e2.y);
+              u[j + 3] = pack_bf16x2(e3.x, e3.y);
+            } else {
+              u[j] = split_pair(e0, u2[j], u3[j]);
+              u[j + 1] = split_pair(e1, u2[j + 1], u3[j + 1]);
+              u[j + 2] = split_pair(e2, u2[j + 2], u3[j + 2]);
+              u[j + 3] = split_pair(e3, u2[j + 3], u3[j + 3]);
+            }
           }
           tmem_st16(tS + ch * 16, u);   // over this thread's own scores, read before
+          if constexpr (PL == 3) {
+            tmem_st16(tS + KT + ch * 16, u2);
+            tmem_st16(tS + KT + 32 + ch * 16, u3);
+          }
         }
       } else {   // by ex2 alone: the polynomial does not reach 0, which hidden keys need
 #pragma unroll 1
         for (int ch = 0; ch < 64; ch += 32) {
-          uint32_t u[16];
+          uint32_t u[16], u2[PL == 3 ? 16 : 1], u3[PL == 3 ? 16 : 1];
           if (last_last - j0 >= ch) {
             float v[32];
             tmem_ld32(tS + ch, v);
@@ -460,13 +515,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
               const float2 x = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), cc, nb);
               const float2 e = make_float2(ch + 2 * j <= lim ? ex2(x.x) : 0.0f, ch + 2 * j + 1 <= lim ? ex2(x.y) : 0.0f);
               s0 = __fadd2_rn(s0, e);
-              u[j] = pack_bf16x2(e.x, e.y);
+              if constexpr (PL == 1) u[j] = pack_bf16x2(e.x, e.y);
+              else u[j] = split_pair(e, u2[j], u3[j]);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) u[j] = 0u;
+            for (int j = 0; j < 16; ++j) {
+              u[j] = 0u;
+              if constexpr (PL == 3) u2[j] = u3[j] = 0u;
+            }
           }
           tmem_st16(tS + (ch >> 1), u);
+          if constexpr (PL == 3) {
+            tmem_st16(tS + KT + (ch >> 1), u2);
+            tmem_st16(tS + KT + 32 + (ch >> 1), u3);
+          }
         }
       }
       l += (s0.x + s1.x) + (s0.y + s1.y);
@@ -486,7 +549,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     if (!aborted) {
       tc_after_sync();
       const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
+      using T = std::conditional_t<PL == 1, __nv_bfloat16, float>;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
 #pragma unroll 1
       for (int ch = 0; ch < kOCols / 32; ++ch) {
         float o[32];
@@ -499,9 +563,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         }
         if (r < my_rows) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                         pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+          for (int j = 0; j < 32; ++j) o[j] *= inv;
+          if constexpr (PL == 1) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                                           pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[ch * 8 + q] = make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]), __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3]));
+          }
         }
       }
       if (p.offset && half == 0 && r < my_rows)   // exp2(c (S + offset)) = P
@@ -520,15 +592,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
 // =================================================================================================
 // WEIGHT
 // =================================================================================================
-template <int DH_>
+template <int DH_, int STAGES, int PL_ = 1>
 struct WeightCfg {
-  static constexpr int DH = DH_;
-  static constexpr int kStages = DH == 64 ? 3 : 2;
-  static constexpr uint32_t kTile = kRows * DH * 2u, kExtra = kRows * 32u;   // and 16 channels more
+  static constexpr int DH = DH_, PL = PL_;
+  static constexpr int kStages = STAGES;
+  static constexpr uint32_t kTile = PL * kRows * DH * 2u, kExtra = kRows * 32u;   // and 16 channels more
   static constexpr uint32_t oQ = kTile + kExtra, kStage = kTile + kExtra;
   static constexpr uint32_t kSmem = oQ + kStages * kStage + 1024u;
   static constexpr int kSoftmax = 256, kThreads = kSoftmax + 64;
   static constexpr uint32_t kTmem = 256;   // two score buffers
+  static constexpr int kCtas = 2 * kSmem > 226 * 1024 ? 1 : 2;
 };
 
 // The row's offset -(m + log2 l) / c enters the scores by an MMA step of 16 channels more: the keys' are three
@@ -553,8 +626,8 @@ struct WeightBars {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
-  constexpr int DH = C::DH, NST = C::kStages;
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
+  constexpr int DH = C::DH, PL = C::PL, NST = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ WeightBars<NST> bars;
@@ -603,7 +676,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       item = pt;
       if (pt.b >= 0 && (pt.q.n + kRows - 1) / kRows > first_tile(pt)) {
         mbar_arrive_expect_tx(&bars.k_full, C::kTile);
-        load_tile<DH, kRows>(smem, &maps.k, hk, pt.k.first + pt.tile * kRows, &bars.k_full);
+        load_tile<DH, kRows, PL>(smem, &maps.k, hk, pt.k.first + pt.tile * kRows, a.total_kv, &bars.k_full);
       }
     }
     __syncwarp();
@@ -641,7 +714,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
       uint8_t* dst = smem + C::oQ + s * C::kStage;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars.q_full[s], C::kTile);
-        load_tile<DH, kRows>(dst, &maps.q, h, qr.first + i0, &bars.q_full[s]);
+        load_tile<DH, kRows, PL>(dst, &maps.q, h, qr.first + i0, a.total_q, &bars.q_full[s]);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -676,7 +749,7 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
           break;
         }
         tc_after_sync();
-        mma_scores<DH, kRows>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
+        mma_scores<DH, kRows, PL>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
         if (elect_one()) mma_f16(tmem + (t & 1) * 128, eK, eQ + s * (C::kStage >> 4), id, 1u);
         commit_one(&bars.s_full[t & 1]);
         commit_one(&bars.q_empty[s]);
@@ -763,26 +836,32 @@ __global__ void __launch_bounds__(C::kThreads, 2) prompt_weight_kernel(PromptPro
   }
 }
 
-// weight += the sums of a group's heads, in head order; blockIdx.y = key/value head
-__global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem p) {
+// =================================================================================================
+// SPLIT: float32 q, k and v (blockIdx.y) into three bfloat16 planes each
+// =================================================================================================
+__global__ void __launch_bounds__(256) prompt_split_kernel(PromptProblem p) {
   grid_dep_trigger();
   grid_dep_wait();
   const spatten_prompt_args& a = p.a;
-  const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
-  if (r >= a.total_kv) return;
-  const int b = owner_of_row(a.cu_kv, a.B, r);
-  if (b < 0) return;
-  const PackedRows kr = packed_rows(a.cu_kv, b, a.total_kv);
-  const int j = r - kr.first;
-  if (kr.bad || j < 0 || j >= kr.n) return;
-  if (j >= a.weight_cap) {
-    report(a.dev_status, SPATTEN_E_INDEX);
-    return;
+  const int t = blockIdx.y;
+  const float* src = static_cast<const float*>(t == 0 ? a.q : (t == 1 ? a.k : a.v));
+  const int64_t ld = t == 0 ? a.q_ld_tok : a.kv_ld_tok;
+  const int row = (t == 0 ? a.H : a.H_kv) * a.d_h / 8;   // octets
+  const int64_t octets = static_cast<int64_t>(t == 0 ? a.total_q : a.total_kv) * row;
+  uint4* dst = reinterpret_cast<uint4*>(p.planes[t]);
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < octets; e += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = octets <= INT32_MAX ? static_cast<int64_t>(static_cast<uint32_t>(e) / static_cast<uint32_t>(row)) : e / row;
+    const float4* x = reinterpret_cast<const float4*>(src + r * ld + (e - r * row) * 8);
+    const float4 u = x[0], v = x[1];
+    uint4 mid, low, hi;
+    hi.x = split_pair(make_float2(u.x, u.y), mid.x, low.x);
+    hi.y = split_pair(make_float2(u.z, u.w), mid.y, low.y);
+    hi.z = split_pair(make_float2(v.x, v.y), mid.z, low.z);
+    hi.w = split_pair(make_float2(v.z, v.w), mid.w, low.w);
+    dst[e] = hi;
+    dst[octets + e] = mid;
+    dst[2 * octets + e] = low;
   }
-  const float* part = p.part + static_cast<int64_t>(hk) * G * a.total_kv + r;
-  float sum = 0.0f;
-  for (int g = 0; g < G; ++g) sum += part[static_cast<int64_t>(g) * a.total_kv];
-  a.weight[static_cast<int64_t>(b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
 }
 
 // =================================================================================================
@@ -829,9 +908,19 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
   }));
   const spatten_prompt_args& a = p.a;
   Maps maps;
-  SPT_TRY(make_map(&maps.q, a.q, O::DH, a.H, a.total_q, a.q_ld_tok));
-  SPT_TRY(make_map(&maps.k, a.k, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
-  SPT_TRY(make_map(&maps.v, a.v, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
+  if constexpr (O::PL == 1) {
+    SPT_TRY(make_map(&maps.q, a.q, O::DH, a.H, a.total_q, a.q_ld_tok));
+    SPT_TRY(make_map(&maps.k, a.k, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
+    SPT_TRY(make_map(&maps.v, a.v, O::DH, a.H_kv, a.total_kv, a.kv_ld_tok));
+  } else {
+    const int64_t hd = static_cast<int64_t>(a.H) * O::DH, hkd = static_cast<int64_t>(a.H_kv) * O::DH;
+    SPT_TRY(make_map(&maps.q, p.planes[0], O::DH, a.H, 3 * a.total_q, hd));
+    SPT_TRY(make_map(&maps.k, p.planes[1], O::DH, a.H_kv, 3 * a.total_kv, hkd));
+    SPT_TRY(make_map(&maps.v, p.planes[2], O::DH, a.H_kv, 3 * a.total_kv, hkd));
+    const int64_t octets = std::max<int64_t>(hd * a.total_q, hkd * a.total_kv) / 8;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_div(octets, 256), 16 * sm_count()));
+    SPT_TRY(launch_chained(prompt_split_kernel, dim3(blocks, 3), dim3(256), 0, st, 1, p));
+  }
   const bool pair_heads = O::NQ == 2 && (a.H / a.H_kv) % 2 == 0;
   const int tile_rows = O::NQ == 2 && !pair_heads ? 256 : 128;
   // a sequence's rows end in at most one partial tile, so this many tiles cover any offsets
@@ -842,19 +931,23 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
   if (!a.weight) return SPATTEN_OK;
   SPT_TRY(launch_chained(prompt_weight_kernel<W>, dim3(static_cast<unsigned>(k_blocks)), dim3(W::kThreads), W::kSmem, st, 1, p, maps));
   if (a.H == a.H_kv) return SPATTEN_OK;
-  return launch_chained(prompt_weight_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(a.total_kv, 256)), a.H_kv), dim3(256), 0, st, 1, p);
+  return prompt_reduce_launch(p, st);
 }
 
 }  // namespace
 
 bool prompt_tc_supported(const spatten_prompt_args& a) {
-  // a tensor map holds row strides below 2^40 bytes
-  return a.dtype == SPATTEN_BF16 && a.total_kv > 0 && a.q_ld_tok < (1LL << 38) && a.kv_ld_tok < (1LL << 38);
+  if (a.total_kv < 1) return false;
+  // a tensor map holds row strides below 2^40 bytes; float32 operands are planes of a block each, 3 blocks of rows
+  return a.dtype == SPATTEN_BF16 ? a.q_ld_tok < (1LL << 38) && a.kv_ld_tok < (1LL << 38)
+                                 : a.total_q <= INT32_MAX / 4 && a.total_kv <= INT32_MAX / 4;
 }
 
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st) {
-  if (p.a.d_h == 64) return launch<OutCfg<64, 1, 64, 4>, WeightCfg<64>>(p, st);
-  return launch<OutCfg<128, 2, 128, 4>, WeightCfg<128>>(p, st);
+  if (p.a.dtype == SPATTEN_BF16)
+    return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 4>, WeightCfg<64, 3>>(p, st) : launch<OutCfg<128, 2, 128, 4>, WeightCfg<128, 2>>(p, st);
+  return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 2, 3>, WeightCfg<64, 1, 3>>(p, st)
+                       : launch<OutCfg<128, 1, 64, 2, 3>, WeightCfg<128, 1, 3>>(p, st);
 }
 
 }  // namespace spt

@@ -368,8 +368,8 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  * A row that sees no key (n_q > n_kv) gets O = 0 and adds nothing.  Sums are made in a fixed order
  * (reruns are bit-identical).  P enters the product with V as bfloat16 for bfloat16 inputs (as the
  * values do), float32 for float32 ones; statistics and sums are float32.
- *  - total_q and total_kv are the rows of the packed blocks; rows outside every sequence are neither
- *    read nor written.  Offsets that decrease or leave [0, total] are reported (SPATTEN_E_INDEX) and
+ *  - total_q and total_kv are the rows of the packed blocks; rows outside every sequence change
+ *    nothing and are not written.  Offsets that decrease or leave [0, total] are reported (SPATTEN_E_INDEX) and
  *    their sequence is taken as empty.
  *  - Infinities and NaN in rows of other sequences, or outside every sequence, change nothing.  Inside
  *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable.

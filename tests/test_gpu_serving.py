@@ -103,6 +103,7 @@ CASES = [  # dtype, d, H, Hk, query rows, key rows
     (BF, 64, 4, 4, [37], [37]), (BF, 128, 8, 2, [1], [1]), (BF, 64, 6, 2, [128, 256, 129, 1, 0, 300], [128, 256, 129, 1, 0, 300]),
     (BF, 128, 4, 1, [257, 33], [257, 33]), (BF, 128, 3, 3, [5, 400, 64], [261, 912, 64]), (BF, 64, 8, 1, [1, 130], [515, 131]),
     (BF, 64, 2, 2, [70, 3, 9], [20, 0, 9]), (BF, 128, 2, 1, [300, 140], [45, 139]), (BF, 128, 8, 8, [700], [700]),
+    (F32, 64, 2, 1, [200, 65, 500], [200, 130, 577]), (F32, 128, 4, 2, [129, 40, 300], [321, 40, 700]),
     (F32, 64, 4, 4, [128, 1, 61], [128, 1, 61]), (F32, 128, 6, 2, [33, 65], [100, 65]), (F32, 64, 2, 1, [40, 5], [7, 0]),
 ]
 
