@@ -8,7 +8,7 @@ that use them (``spatten_prompt_attention``, ``spatten_kv4_append`` / ``_attenti
     o = st.step(q, k, v)                   # one token per sequence: append, attend
     o = st.resume(q, k, v, cu, cu_kv, rows)   # prompts that go on over the cached rows
 
-Calls run on torch's current stream.  The counts live on the device, so ``step`` and ``evict`` can be
+Calls run on the state's GPU, on torch's current stream there.  The counts live on the device, so ``step`` and ``evict`` can be
 captured in a CUDA graph and replayed.
 """
 import torch
@@ -49,6 +49,10 @@ class KV4State:
             raise ValueError("k and v are [rows, H_kv, d_h] alike, with the heads of a row contiguous")
         if k.dtype != v.dtype:
             raise TypeError("k and v have one dtype")
+        if cu is not None and S._i32_vector(cu, "cu") != self.B + 1:
+            raise ValueError("cu has one entry more than there are sequences")
+        if cu is None and k.shape[0] != self.B:
+            raise ValueError("without cu there is one row per sequence")
         S.kv4_append(self.cache, k, v, S._row_stride(k), k.shape[0], self.len, self.len, self.seen, self.seen, cu=cu,
                      dev_status=self.status)
 

@@ -157,9 +157,10 @@ def ptr(t) -> int | None:
     """Device address of a torch tensor (None passes through; ints are taken as addresses)."""
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:
         return t
-    return t.data_ptr()
 
 
 _current_stream = None
@@ -177,13 +178,18 @@ def _stream(stream) -> int | None:
     return _current_stream()
 
 
+_dtype_codes: dict = {}   # torch dtype -> code, filled as dtypes are met (a lookup in `torch` costs 0.1 us a call)
+
+
 def dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        import torch
+        code = {torch.float32: F32, torch.bfloat16: BF16}.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        _dtype_codes[t.dtype] = code
+    return code
 
 
 # ---- calls --------------------------------------------------------------------------------------
@@ -264,6 +270,43 @@ def make_cfg(mode, B, T, D, H, d_h, L, dtype, token_keep, head_keep, quant, thet
 
 
 # ---- prompts and the 4-bit cache --------------------------------------------------------------------
+def _one_device(*tensors) -> int:
+    """The GPU (-1: host memory) that all of a call's tensors are on."""
+    on = {t.get_device() for t in tensors if t is not None}
+    if len(on) > 1:
+        raise ValueError("the tensors of a call are on one device")
+    return on.pop() if on else -1
+
+
+def _check_device(device, *tensors):
+    """What a call is given besides its cache (tensors, or addresses, which are not looked at)."""
+    for t in tensors:
+        if t is not None and type(t) is not int and t.get_device() != device:
+            raise ValueError("the tensors of a call are on one device")
+
+
+_get_device = None
+
+
+def _run(fn, name, device, stream, *args):
+    """One call on `device`, which becomes the current one meanwhile if it is not."""
+    global _get_device
+    if device < 0:
+        raise ValueError(f"{name}: the tensors are not on a GPU")
+    if _get_device is None:
+        import torch
+        torch.cuda.init()
+        _get_device = torch._C._cuda_getDevice
+    if device == _get_device():
+        status = fn(*args, _stream(stream))
+    else:
+        import torch
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    if status != OK:
+        raise SpattenError(status, name)
+
+
 def make_prompt_args(q, k, v, o, cu_q, cu_kv=None, weight=None, sm_scale=0.0, dev_status=None,
                      kernel=ATTN_AUTO) -> prompt_args:
     """Arguments of ``prompt_attention`` from torch tensors: q, o [rows, H, d_h] and k, v [rows, H_kv, d_h]
@@ -277,6 +320,7 @@ def make_prompt_args(q, k, v, o, cu_q, cu_kv=None, weight=None, sm_scale=0.0, de
     if not (q.dtype == k.dtype == v.dtype == o.dtype):
         raise TypeError("q, k, v and o have one dtype")
     a = prompt_args()
+    a._device = _one_device(q, k, v, o, cu_q, cu_kv, weight, dev_status)
     a.B, a.H, a.H_kv, a.d_h = _i32_vector(cu_q, "cu_q") - 1, q.shape[1], k.shape[1], q.shape[2]
     if cu_kv is not None and _i32_vector(cu_kv, "cu_kv") != a.B + 1:
         raise ValueError("cu_kv and cu_q have the same length")
@@ -314,7 +358,7 @@ def prompt_workspace_size(args: prompt_args) -> int:
 
 
 def prompt_attention(args: prompt_args, ws=None, ws_bytes: int = 0, stream=None):
-    check(lib.spatten_prompt_attention(C.byref(args), ptr(ws), ws_bytes, _stream(stream)), "spatten_prompt_attention")
+    _run(lib.spatten_prompt_attention, "spatten_prompt_attention", args._device, stream, C.byref(args), ptr(ws), ws_bytes)
 
 
 def make_kv4_cache(k_codes, k_scale, v_codes, v_scale, weight=None, pos=None) -> kv4_cache:
@@ -329,20 +373,26 @@ def make_kv4_cache(k_codes, k_scale, v_codes, v_scale, weight=None, pos=None) ->
             raise TypeError(f"a cache tensor is not a contiguous {dt} {(B, H, cap) + tail}")
     c = kv4_cache(B, H, 2 * half, cap, ptr(k_codes), ptr(k_scale), ptr(v_codes), ptr(v_scale), ptr(weight), ptr(pos))
     c._keep = (k_codes, k_scale, v_codes, v_scale, weight, pos)
+    c._device, c._ref = _one_device(*c._keep), C.byref(c)
     return c
+
+
+_append_fn, _read_fn = lib.spatten_kv4_append, lib.spatten_kv4_read
 
 
 def kv4_append(cache: kv4_cache, k, v, ld_tok, total, len, len_out, seen=None, seen_out=None, cu=None, dtype=None,
                dev_status=None, stream=None):
     dt = dtype_code(k) if dtype is None else dtype
-    check(lib.spatten_kv4_append(C.byref(cache), ptr(k), ptr(v), dt, ld_tok, total, ptr(cu), ptr(len), ptr(len_out),
-                                 ptr(seen), ptr(seen_out), ptr(dev_status), _stream(stream)), "spatten_kv4_append")
+    _check_device(cache._device, k, v, len, len_out, cu)
+    _run(_append_fn, "spatten_kv4_append", cache._device, stream, cache._ref, ptr(k), ptr(v), dt, ld_tok, total, ptr(cu), ptr(len),
+         ptr(len_out), ptr(seen), ptr(seen_out), ptr(dev_status))
 
 
 def kv4_read(cache: kv4_cache, cu, total, k_out, v_out, ld_tok, row0=None, dtype=None, dev_status=None, stream=None):
     dt = dtype_code(k_out if k_out is not None else v_out) if dtype is None else dtype
-    check(lib.spatten_kv4_read(C.byref(cache), ptr(cu), ptr(row0), total, ptr(k_out), ptr(v_out), dt, ld_tok,
-                               ptr(dev_status), _stream(stream)), "spatten_kv4_read")
+    _check_device(cache._device, cu, k_out, v_out)
+    _run(_read_fn, "spatten_kv4_read", cache._device, stream, cache._ref, ptr(cu), ptr(row0), total, ptr(k_out), ptr(v_out), dt,
+         ld_tok, ptr(dev_status))
 
 
 def make_kv4_attn_args(cache: kv4_cache, q, o, len, n_max, update_weight=True, sm_scale=0.0,
@@ -361,6 +411,7 @@ def make_kv4_attn_args(cache: kv4_cache, q, o, len, n_max, update_weight=True, s
     a.o, a.o_ld, a.len, a.n_max, a.sm_scale = ptr(o), _row_stride(o), ptr(len), n_max, sm_scale
     a.update_weight, a.dev_status = int(update_weight), ptr(dev_status)
     a._keep = (cache, q, o, len, dev_status)
+    a._device = _one_device(cache._keep[0], q, o, len, dev_status)
     return a
 
 
@@ -369,7 +420,7 @@ def kv4_attention_workspace_size(args: kv4_attn_args) -> int:
 
 
 def kv4_attention(args: kv4_attn_args, ws, ws_bytes: int, stream=None):
-    check(lib.spatten_kv4_attention(C.byref(args), ptr(ws), ws_bytes, _stream(stream)), "spatten_kv4_attention")
+    _run(lib.spatten_kv4_attention, "spatten_kv4_attention", args._device, stream, C.byref(args), ptr(ws), ws_bytes)
 
 
 def kv4_evict_workspace_size(cache: kv4_cache, n_max: int, keep: int) -> int:
@@ -378,5 +429,6 @@ def kv4_evict_workspace_size(cache: kv4_cache, n_max: int, keep: int) -> int:
 
 def kv4_evict(src: kv4_cache, dst: kv4_cache, len, len_out, seen, n_max, keep, recent, ws, ws_bytes: int,
               dev_status=None, stream=None):
-    check(lib.spatten_kv4_evict(C.byref(src), C.byref(dst), ptr(len), ptr(len_out), ptr(seen), n_max, keep, recent,
-                                ptr(ws), ws_bytes, ptr(dev_status), _stream(stream)), "spatten_kv4_evict")
+    _check_device(src._device, dst._keep[0], len, len_out, ws)
+    _run(lib.spatten_kv4_evict, "spatten_kv4_evict", src._device, stream, src._ref, dst._ref, ptr(len), ptr(len_out), ptr(seen),
+         n_max, keep, recent, ptr(ws), ws_bytes, ptr(dev_status))

@@ -187,6 +187,24 @@ def test_binding_checks_tensors(S):
         S.make_kv4_attn_args(c, row, row, cu, 7)
 
 
+def test_host_tensors_are_refused(S):
+    """Tensors in host memory describe a call, but the call itself refuses them."""
+    q, k = torch.zeros(5, 4, 64), torch.zeros(5, 2, 64)
+    cu, n = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        S.prompt_attention(S.make_prompt_args(q, k, k, q, cu))
+    codes, scale, w = torch.zeros(1, 2, 7, 32, dtype=torch.uint8), torch.zeros(1, 2, 7, 2, dtype=torch.bfloat16), torch.zeros(1, 2, 7)
+    c = S.make_kv4_cache(codes, scale, codes, scale, w)
+    with pytest.raises(ValueError):
+        S.kv4_append(c, k, k, 128, 5, n, n, cu=cu)
+    with pytest.raises(ValueError):
+        S.kv4_read(c, cu, 5, k, k, 128)
+    with pytest.raises(ValueError):
+        S.kv4_attention(S.make_kv4_attn_args(c, q[:1], q[:1], n, 7), w, 28)
+    with pytest.raises(ValueError):
+        S.kv4_evict(c, c, n, n, None, 7, 3, 0, w, 28)
+
+
 # ---- the plain forms --------------------------------------------------------------------------------
 def test_plain_quantizer_by_hand():
     x = np.zeros(64, np.float32)
