@@ -48,9 +48,14 @@ template <int DH> constexpr int kTileKeys = 2048 / DH;
 
 struct AttnArgs {
   spatten_kv4_attn_args a;
-  float* x;         // ws [B][H_kv][C][heads][x_ld] scores, or NULL: in shared memory
-  int32_t x_ld;     // floats between the heads' scores of one CTA's keys
+  float* x;         // ws scores: [B][H_kv][C][heads][x_ld] of clusters (NULL: in shared memory), [B][H_kv][heads][x_ld] of
+                    // the split form (NULL: no weights)
+  int64_t x_ld;     // floats between the heads' scores
   int32_t heads;    // min(H / H_kv, kMaxHeads)
+  // the split form: CTAs, first head of the pass, and each segment's maxima, sums and outputs
+  int32_t ctas, h0;
+  float2* part_ml;  // ws [ctas + B H_kv][heads]
+  float* part_o;    // ws [ctas + B H_kv][heads][d_h]
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -266,7 +271,7 @@ struct Warp {
   // xs: where this lane's scores go (keys gid and gid + 8 of heads 2t and, x_ld behind, 2t + 1; 8 x_ld per
   // column), or NULL.  left: keys there are, counted from key gid (FULL: all).
   template <bool FULL>
-  __device__ __forceinline__ void tile16(const uint8_t* sk, const uint8_t* sv, const uint8_t* ss, float* xs, int x_ld, int heads,
+  __device__ __forceinline__ void tile16(const uint8_t* sk, const uint8_t* sv, const uint8_t* ss, float* xs, int64_t x_ld, int heads,
                                          int left, int lane) {
     const int t = lane & 3;
     uint32_t kw[2][G32], ks[2][G32 / 2], vs[2][G32 / 2];
@@ -409,11 +414,170 @@ struct Warp {
   }
 };
 
+// A warp's way through a run of n rows of the cache from row0 on: the CTA's kWarps warps take its tiles in turn.
+template <int DH>
+struct Run {
+  static constexpr int TK = kTileKeys<DH>, G32 = DH / kKv4Group;
+  static constexpr int kPieces = DH / 32;   // 16-byte pieces of a row's codes
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  const spatten_kv4_cache& c;
+  uint8_t* ring;
+  int warp, lane;
+  // this lane's pieces of the tile to copy next: where they come from, where they go, and the run's rows from that
+  // tile on.  (Addresses made anew for every tile were an eighth of the kernel's instructions.)
+  const uint8_t *pk, *pv, *ps, *pt;
+  uint32_t d_code, d_v0, d_v1, d_scale, d_stage;
+  int to_copy, rows;
+  int lk, lv, ls;   // its first codes and scales of a staged tile
+
+  __device__ __forceinline__ Run(const spatten_kv4_cache& cache, uint8_t* rings, int warp_, int lane_)
+      : c(cache), ring(rings + warp_ * kRingBytes), warp(warp_), lane(lane_) {
+    const int r = lane / kPieces, ch = lane % kPieces, gid = lane >> 2, t = lane & 3;
+    d_code = smem_addr(ring) + lane * 16;
+    d_v0 = smem_addr(ring) + 1024 + v_offset<DH>(r, ch * 16);
+    d_v1 = smem_addr(ring) + 1024 + v_offset<DH>(r + 32 / kPieces, ch * 16);
+    d_scale = smem_addr(ring) + 2048 + lane * (DH / 16);
+    lk = gid * (DH / 2) + t * (DH / 8);
+    lv = 1024 + v_offset<DH>(2 * t, gid * (DH / 16));   // slot t holds V's row 2t, slot 4 + t row 2t + 1
+    ls = 2048 + gid * (DH / 16);
+  }
+  __device__ __forceinline__ void load() {   // copies the warp's next tile, if there is one
+    const uint32_t d = d_stage;
+    if (to_copy >= TK) {
+      cp_async<16>(d_code + d, pk);
+      cp_async<16>(d_code + d + 512, pk + 512);
+      cp_async<16>(d_v0 + d, pv);
+      cp_async<16>(d_v1 + d, pv + 512);
+      if constexpr (DH == 128) {
+        cp_async<8>(d_scale + d, ps);
+      } else {
+        cp_async<4>(d_scale + d, ps);
+        cp_async<4>(d_scale + d + 128, pt);
+      }
+    } else if (to_copy > 0) {   // rows past the keys are zero-filled, not read
+      const int r = lane / kPieces;
+      const bool ok0 = r < to_copy, ok1 = r + 32 / kPieces < to_copy, oks = (DH == 128 ? lane & 15 : lane) < to_copy;
+      cp_async_if<16>(d_code + d, pk, c.k_codes, ok0);
+      cp_async_if<16>(d_code + d + 512, pk + 512, c.k_codes, ok1);
+      cp_async_if<16>(d_v0 + d, pv, c.v_codes, ok0);
+      cp_async_if<16>(d_v1 + d, pv + 512, c.v_codes, ok1);
+      if constexpr (DH == 128) {
+        cp_async_if<8>(d_scale + d, ps, c.k_scale, oks);
+      } else {
+        cp_async_if<4>(d_scale + d, ps, c.k_scale, oks);
+        cp_async_if<4>(d_scale + d + 128, pt, c.v_scale, oks);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    pk += kWarps * TK * (DH / 2);
+    pv += kWarps * TK * (DH / 2);
+    ps += kWarps * TK * G32 * 2;
+    if constexpr (DH == 64) pt += kWarps * TK * G32 * 2;
+    to_copy -= kWarps * TK;
+    d_stage = d_stage == kRingBytes - kStageBytes ? 0 : d_stage + kStageBytes;
+  }
+  __device__ __forceinline__ void start(int64_t row0, int n) {
+    const int64_t at = (row0 + warp * TK) * (DH / 2) + lane * 16, as = (row0 + warp * TK + (DH == 128 ? lane & 15 : lane)) * G32;
+    pk = c.k_codes + at;
+    pv = c.v_codes + at;
+    ps = reinterpret_cast<const uint8_t*>((DH == 64 || lane < 16 ? c.k_scale : c.v_scale) + as);
+    pt = reinterpret_cast<const uint8_t*>(c.v_scale + as);   // 64 channels
+    rows = to_copy = n - warp * TK;
+    d_stage = 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load();
+  }
+  // x: the scores of the run's first key, or NULL
+  template <class W>
+  __device__ __forceinline__ void process(W& w, float* x, int64_t x_ld, int heads) {
+    float* xt = x ? x + 2 * (lane & 3) * x_ld + warp * TK + (lane >> 2) : nullptr;
+    const uint8_t* st = ring;
+    for (int left = rows; left > 0; left -= kWarps * TK) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();   // every lane's copies have landed, and every lane is done with the previous tile
+      load();
+      if (left >= TK) {
+#pragma unroll
+        for (int sub = 0; sub < TK / 16; ++sub)
+          w.template tile16<true>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads, 0, lane);
+      } else {
+#pragma unroll 1
+        for (int sub = 0; sub < TK / 16; ++sub)
+          w.template tile16<false>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads,
+                                   left - 16 * sub - (lane >> 2), lane);
+      }
+      if (xt) xt += kWarps * TK;
+      st = st == ring + (kRingBytes - kStageBytes) ? ring : st + kStageBytes;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+};
+
+// The warps' sums over their common maxima, in warp order: ml(h, maximum, sum) by the threads that `by` gives a
+// head (-1: none), o(e, sum) for the heads' channels e; between() runs before the block meets.
+template <int DH, int NH, class W, typename By, typename Between, typename Ml, typename O>
+__device__ __forceinline__ void merge_warps(const W& w, uint8_t* smem, float (*s_m)[NH * 8], float (*s_l)[NH * 8], int heads, By by,
+                                            Between between, Ml ml, O o) {
+  constexpr int kPart = ring_bytes(DH, NH) / kWarps / 4;   // floats of a warp's share of the rings
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float l = w.l[nh][k];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (gid == 0) {
+        s_m[warp][nh * 8 + 2 * t + k] = w.maximum(nh, k);
+        s_l[warp][nh * 8 + 2 * t + k] = l;
+      }
+    }
+  __syncwarp();
+  float* part = reinterpret_cast<float*>(smem);   // [warp][head][channel]: over the warp's own ring (and, 16 heads, more)
+  if (ring_bytes(DH, NH) > kWarps * kStages * kStageBytes) __syncthreads();   // which others may still read
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int h = nh * 8 + 2 * t + k;
+      if (h < heads) {
+        float* dst = part + warp * kPart + h * DH + 4 * gid;
+#pragma unroll
+        for (int j = 0; j < DH / 32; ++j)   // channels 32 j + 4 gid .. + 3
+          *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(w.o[nh][2 * j][k], w.o[nh][2 * j][k + 2], w.o[nh][2 * j + 1][k], w.o[nh][2 * j + 1][k + 2]);
+      }
+    }
+  between();
+  __syncthreads();
+  float fac[kWarps];
+  auto factors = [&](int h) {   // of the warps' sums; the maximum
+    float m[kWarps], mx = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) mx = fmaxf(mx, m[v] = s_m[v][h]);
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) fac[v] = ex2(m[v] - (mx == -INFINITY ? 0.0f : mx));
+    return mx;
+  };
+  if (const int h = by(tid); h >= 0) {
+    const float mx = factors(h);
+    float l = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][h], fac[v], l);
+    ml(h, mx, l);
+  }
+  for (int e = tid; e < heads * DH; e += kThreads) {
+    factors(e / DH);
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v = fmaf(part[k * kPart + e], fac[k], v);
+    o(e, v);
+  }
+}
+
 template <int DH, int NH, typename T>
 __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) kv4_attn_kernel(AttnArgs args) {
   using W = Warp<DH, NH, T>;
   constexpr int TK = W::TK, G32 = W::G32, kHeads = NH * 8;
-  constexpr int kPart = ring_bytes(DH, NH) / kWarps / 4;   // floats of a warp's share of the rings
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings (later their sums), then the scores
   __shared__ __align__(16) typename W::Query query[NH];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
@@ -429,7 +593,6 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   const spatten_kv4_attn_args& a = args.a;
   const spatten_kv4_cache& c = a.cache;
   const int hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gid = lane >> 2, t = lane & 3;
   const int group = a.H / c.H_kv;
   // the query's loads go out first: what follows them waits for the length
   typename W::Raw raw;
@@ -439,65 +602,16 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   const int run = (((n_all + C - 1) / C) + TK - 1) / TK * TK;   // keys per CTA
   const int first = min(n_all, rank * run), n = min(run, n_all - first);
   const int64_t row0 = (static_cast<int64_t>(b) * c.H_kv + hk) * c.cap + first;
-  const int tiles = (n + TK - 1) / TK;
-  uint8_t* ring = smem + warp * kStages * kStageBytes;
-  const int x_ld = args.x_ld;
-  float* x = args.x ? args.x + ((static_cast<int64_t>(b) * c.H_kv + hk) * C + rank) * args.heads * static_cast<int64_t>(x_ld)
+  const int64_t x_ld = args.x_ld;
+  float* x = args.x ? args.x + ((static_cast<int64_t>(b) * c.H_kv + hk) * C + rank) * args.heads * x_ld
                     : reinterpret_cast<float*>(smem + ring_bytes(DH, NH));
   if (!a.update_weight) x = nullptr;
 
-  // this lane's share of a tile's copies: two pieces of 16 bytes of each tensor's codes, and scales
-  constexpr int kPieces = DH / 32;
-  const int r_a = lane / kPieces, ch = lane % kPieces;
-  const int64_t at0 = (row0 + warp * TK) * (DH / 2) + lane * 16;
-  const int64_t as0 = (row0 + warp * TK + (DH == 128 ? lane & 15 : lane)) * G32;
-  const uint16_t* gs0 = (DH == 64 || lane < 16 ? c.k_scale : c.v_scale) + as0;
-  const uint32_t d_code = smem_addr(ring) + lane * 16, d_v0 = smem_addr(ring) + 1024 + v_offset<DH>(r_a, ch * 16),
-                 d_v1 = smem_addr(ring) + 1024 + v_offset<DH>(r_a + 32 / kPieces, ch * 16),
-                 d_scale = smem_addr(ring) + 2048 + lane * (DH / 16);
-  // copies the warp's i-th tile
-  auto load = [&](int i, int stage) {
-    const uint32_t d = stage * kStageBytes;
-    const int64_t step = static_cast<int64_t>(i) * (kWarps * TK);
-    const uint8_t *pk = c.k_codes + at0 + step * (DH / 2), *pv = c.v_codes + at0 + step * (DH / 2);
-    const uint16_t* ps = gs0 + step * G32;
-    const int left = n - (i * kWarps + warp) * TK;
-    if (left >= TK) {
-      cp_async<16>(d_code + d, pk);
-      cp_async<16>(d_code + d + 512, pk + 512);
-      cp_async<16>(d_v0 + d, pv);
-      cp_async<16>(d_v1 + d, pv + 512);
-      if constexpr (DH == 128) {
-        cp_async<8>(d_scale + d, ps);
-      } else {
-        cp_async<4>(d_scale + d, ps);
-        cp_async<4>(d_scale + d + 128, c.v_scale + as0 + step * G32);
-      }
-    } else {   // rows past the keys are zero-filled, not read
-      const bool ok0 = r_a < left, ok1 = r_a + 32 / kPieces < left, oks = (DH == 128 ? lane & 15 : lane) < left;
-      cp_async_if<16>(d_code + d, pk, c.k_codes, ok0);
-      cp_async_if<16>(d_code + d + 512, pk + 512, c.k_codes, ok1);
-      cp_async_if<16>(d_v0 + d, pv, c.v_codes, ok0);
-      cp_async_if<16>(d_v1 + d, pv + 512, c.v_codes, ok1);
-      if constexpr (DH == 128) {
-        cp_async_if<8>(d_scale + d, ps, c.k_scale, oks);
-      } else {
-        cp_async_if<4>(d_scale + d, ps, c.k_scale, oks);
-        cp_async_if<4>(d_scale + d + 128, c.v_scale + as0 + step * G32, c.v_scale, oks);
-      }
-    }
-  };
-  // this lane's first codes and scales of a staged tile (slot t holds V's row 2t, slot 4 + t row 2t + 1)
-  const int lk = gid * (DH / 2) + t * (DH / 8), lv = 1024 + v_offset<DH>(2 * t, gid * (DH / 16)), ls = 2048 + gid * (DH / 16);
-
+  Run<DH> way(c, smem, warp, lane);
   if (C > 1) cluster.barrier_arrive();   // this CTA runs: its shared memory can be written
   for (int h0 = 0; h0 < group; h0 += kHeads) {
     const int heads = min(kHeads, group - h0);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (warp + kWarps * i < tiles) load(i, i);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+    way.start(row0, n);
     if (warp < W::kPrepareWarps) {
       if (h0) raw.load(qrow + static_cast<int64_t>(h0) * DH, warp / G32, heads, lane);
       W::prepare(query[warp / G32], raw, warp % G32, a.sm_scale, lane);
@@ -505,85 +619,16 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
     __syncthreads();
     W w;
     w.init(query, lane);
-    float* xs = x ? x + 2 * t * x_ld + gid : nullptr;
-    for (int tile = warp, i = 0; tile < tiles; tile += kWarps, ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();   // every lane's copies have landed, and every lane is done with the previous tile
-      if (tile + kWarps * (kStages - 1) < tiles) load(i + kStages - 1, (i + kStages - 1) % kStages);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint8_t* st = ring + (i % kStages) * kStageBytes;
-      const int key0 = tile * TK;
-      float* xt = xs ? xs + key0 : nullptr;
-      if (n - key0 >= TK) {
-#pragma unroll
-        for (int sub = 0; sub < TK / 16; ++sub)
-          w.template tile16<true>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads, 0, lane);
-      } else {
-#pragma unroll 1
-        for (int sub = 0; sub < TK / 16; ++sub)
-          w.template tile16<false>(st + lk + sub * 512, st + lv + sub * 512, st + ls + sub * 64, xt ? xt + 16 * sub : nullptr, x_ld, heads,
-                                   n - key0 - 16 * sub - gid, lane);
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-
-    // the warps' sums, over their common maximum, in warp order
-#pragma unroll
-    for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float l = w.l[nh][k];
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (gid == 0) {
-          s_m[warp][nh * 8 + 2 * t + k] = w.maximum(nh, k);
-          s_l[warp][nh * 8 + 2 * t + k] = l;
-        }
-      }
-    __syncwarp();
-    float* part = reinterpret_cast<float*>(smem);   // [warp][head][channel]: over the warp's own ring (and, 16 heads, more)
-    if (ring_bytes(DH, NH) > kWarps * kStages * kStageBytes) __syncthreads();   // which others may still read
-#pragma unroll
-    for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int h = nh * 8 + 2 * t + k;
-        if (h < heads) {
-          float* dst = part + warp * kPart + h * DH + 4 * gid;
-#pragma unroll
-          for (int j = 0; j < G32; ++j)   // channels 32 j + 4 gid .. + 3
-            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(w.o[nh][2 * j][k], w.o[nh][2 * j][k + 2], w.o[nh][2 * j + 1][k], w.o[nh][2 * j + 1][k + 2]);
-        }
-      }
-    if (C > 1 && h0 == 0) cluster.barrier_wait();   // every CTA of the cluster runs
-    __syncthreads();
-    // the maximum of a head over the CTA's warps, and the factors of their sums
-    auto warp_factors = [&](int h, float* fac) {
-      float m[kWarps], mx = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) mx = fmaxf(mx, m[v] = s_m[v][h]);
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) fac[v] = ex2(m[v] - (mx == -INFINITY ? 0.0f : mx));
-      return mx;
-    };
-    float fac[kWarps];
-    if (tid < heads * C) {   // maxima and sums to every CTA
-      const int h = tid % heads;
-      const float mx = warp_factors(h, fac);
-      float l = 0.0f;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) l = fmaf(s_l[v][h], fac[v], l);
-      *cluster.map_shared_rank(&in_ml[rank][h], tid / heads) = make_float2(mx, l);
-    }
+    way.process(w, x, x_ld, heads);
     const int share = heads * DH / C;   // the outputs that a CTA adds up
-    for (int e = tid; e < heads * DH; e += kThreads) {
-      warp_factors(e / DH, fac);
-      float v = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) v = fmaf(part[k * kPart + e], fac[k], v);
-      const int to = e / share;
-      *cluster.map_shared_rank(&in_o[rank * share + (e - to * share)], to) = v;
-    }
+    merge_warps<DH, NH>(
+        w, smem, s_m, s_l, heads, [&](int i) { return i < heads * C ? i % heads : -1; },   // maxima and sums to every CTA
+        [&]() { if (C > 1 && h0 == 0) cluster.barrier_wait(); },                           // which all run by now
+        [&](int h, float mx, float l) { *cluster.map_shared_rank(&in_ml[rank][h], tid / heads) = make_float2(mx, l); },
+        [&](int e, float v) {
+          const int to = e / share;
+          *cluster.map_shared_rank(&in_o[rank * share + (e - to * share)], to) = v;
+        });
     if (C > 1) cluster.sync();
     else __syncthreads();
     // the cluster's sums, in rank order
@@ -641,6 +686,184 @@ __global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) k
   }
 }
 
+// ---- the split form: more keys than one wave of clusters holds ----------------------------------------
+// All tiles of all (sequence, head) pairs, in order, are dealt to the CTAs in equal runs (two CTAs an SM; a run of
+// one pair is a segment), so that no CTA waits for others and the work is even whatever the lengths are.  A CTA's
+// segment of pair p leaves its maxima, sums and outputs in slot CTA + p; the scores go to the workspace.  A second
+// kernel adds up and makes the weights.
+struct Deal {
+  int64_t total;   // tiles
+  int N;
+  __device__ __forceinline__ int64_t begin(int cta) const { return cta * total / N; }
+};
+template <int TK>
+__device__ __forceinline__ int tiles_of(const spatten_kv4_attn_args& a, int b) {
+  const int n = b < a.cache.B ? max(0, min(a.n_max, a.len[b])) : 0;
+  return (n + TK - 1) / TK;
+}
+// tiles of sequences b < end, per head; whole warps
+template <int TK>
+__device__ __forceinline__ int64_t tiles_before(const spatten_kv4_attn_args& a, int end) {
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < end; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    sum += __reduce_add_sync(0xffffffffu, b < end ? tiles_of<TK>(a, b) : 0);
+  }
+  return sum;
+}
+
+template <int DH, int NH, typename T>
+__global__ void __launch_bounds__(kThreads, NH == 2 && sizeof(T) == 4 ? 1 : 2) kv4_attn_split_kernel(AttnArgs args) {
+  using W = Warp<DH, NH, T>;
+  constexpr int TK = W::TK, G32 = W::G32, kHeads = NH * 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) typename W::Query query[NH];
+  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+  grid_dep_trigger();
+  grid_dep_wait();
+  const spatten_kv4_attn_args& a = args.a;
+  const spatten_kv4_cache& c = a.cache;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.H / c.H_kv, heads = min(kHeads, group - args.h0);
+  if (blockIdx.x == 0 && args.h0 == 0)
+    for (int b = tid; b < c.B; b += kThreads) clamp_len(a.len[b], a.n_max, a.dev_status);   // reports
+  const Deal deal{tiles_before<TK>(a, c.B) * c.H_kv, static_cast<int>(gridDim.x)};
+  int64_t at = deal.begin(blockIdx.x);
+  const int64_t end = deal.begin(blockIdx.x + 1);
+  if (at == end) return;
+  // the sequence, head and tile of the first
+  int b = 0, hk = 0, t0 = 0;
+  {
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int mine = tiles_of<TK>(a, b0 + lane);
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + static_cast<int64_t>(inc) * c.H_kv > at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        const int tiles = __shfl_sync(0xffffffffu, mine, l);
+        const int64_t in = at - before - static_cast<int64_t>(__shfl_sync(0xffffffffu, inc - mine, l)) * c.H_kv;
+        b = b0 + l;
+        hk = static_cast<int>(in / tiles);
+        t0 = static_cast<int>(in - static_cast<int64_t>(hk) * tiles);
+        break;
+      }
+      before += static_cast<int64_t>(__shfl_sync(0xffffffffu, inc, 31)) * c.H_kv;
+    }
+  }
+  Run<DH> way(c, smem, warp, lane);
+  while (at < end) {
+    const int n_all = max(0, min(a.n_max, a.len[b])), tiles = (n_all + TK - 1) / TK;
+    if (t0 < tiles) {
+      const int count = static_cast<int>(min(static_cast<int64_t>(tiles - t0), end - at));
+      const int64_t pair = static_cast<int64_t>(b) * c.H_kv + hk;
+      way.start(pair * c.cap + static_cast<int64_t>(t0) * TK, min(n_all - t0 * TK, count * TK));
+      if (warp < W::kPrepareWarps) {
+        typename W::Raw raw;
+        raw.load(static_cast<const T*>(a.q) + b * a.q_ld + (static_cast<int64_t>(hk) * group + args.h0) * DH, warp / G32, heads, lane);
+        W::prepare(query[warp / G32], raw, warp % G32, a.sm_scale, lane);
+      }
+      __syncthreads();
+      W w;
+      w.init(query, lane);
+      way.process(w, args.x ? args.x + pair * args.heads * args.x_ld + static_cast<int64_t>(t0) * TK : nullptr, args.x_ld, heads);
+      const int64_t slot = (blockIdx.x + pair) * args.heads;
+      merge_warps<DH, NH>(
+          w, smem, s_m, s_l, heads, [&](int i) { return i < heads ? i : -1; }, []() {},
+          [&](int h, float mx, float l) { args.part_ml[slot + h] = make_float2(mx, l); },
+          [&](int e, float v) { args.part_o[slot * DH + e] = v; });
+      __syncthreads();   // the rings and the query are free again
+      at += count;
+    }
+    t0 = 0;
+    if (++hk == c.H_kv) hk = 0, ++b;
+  }
+}
+
+constexpr int kFinishKeys = 4 * kThreads;
+template <int DH, typename T>
+__global__ void __launch_bounds__(kThreads) kv4_attn_finish_kernel(AttnArgs args) {
+  constexpr int TK = kTileKeys<DH>;
+  __shared__ float2 f[kMaxHeads];   // maxima, and sums inverted
+  __shared__ int first_cta, ctas;
+  __shared__ int64_t total;
+  grid_dep_trigger();
+  grid_dep_wait();
+  const spatten_kv4_attn_args& a = args.a;
+  const spatten_kv4_cache& c = a.cache;
+  const int hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, group = a.H / c.H_kv, heads = min(args.heads, group - args.h0);
+  const int n = max(0, min(a.n_max, a.len[b])), blocks = min(static_cast<int>(gridDim.x), max(1, (n + kFinishKeys - 1) / kFinishKeys));
+  if (blockIdx.x >= blocks) return;
+  const int64_t pair = static_cast<int64_t>(b) * c.H_kv + hk;
+  if (tid < 32) {   // the CTAs that had tiles of this pair
+    const Deal deal{tiles_before<TK>(a, c.B) * c.H_kv, args.ctas};
+    const int tiles = (n + TK - 1) / TK;
+    const int64_t from = tiles_before<TK>(a, b) * c.H_kv + static_cast<int64_t>(hk) * tiles;
+    if (tid == 0) {
+      int i = 0, k = 0;
+      if (tiles) {
+        i = static_cast<int>(from * args.ctas / deal.total);
+        while (deal.begin(i + 1) <= from) ++i;
+        while (deal.begin(i) > from) --i;
+        while (i + k < args.ctas && deal.begin(i + k) < from + tiles) ++k;
+      }
+      first_cta = i;
+      ctas = k;
+      total = deal.total;
+    }
+  }
+  __syncthreads();
+  // with fewer tiles than CTAs some of these have none, and no slot: those whose runs are empty
+  const int64_t slot0 = (first_cta + pair) * args.heads;
+  const Deal deal{total, args.ctas};
+  auto has = [&](int k) { return total >= args.ctas || deal.begin(first_cta + k + 1) > deal.begin(first_cta + k); };
+  if (tid < heads) {
+    float mx = -INFINITY, l = 0.0f;
+    for (int k = 0; k < ctas; ++k)
+      if (has(k)) mx = fmaxf(mx, args.part_ml[slot0 + k * args.heads + tid].x);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    for (int k = 0; k < ctas; ++k)
+      if (has(k)) {
+        const float2 ml = args.part_ml[slot0 + k * args.heads + tid];
+        l = fmaf(ml.y, ex2(ml.x - base), l);
+      }
+    f[tid] = make_float2(base, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));   // an empty sequence gives 0, NaN stays
+  }
+  __syncthreads();
+  for (int e = blockIdx.x * kThreads + tid; e < heads * DH; e += blocks * kThreads) {
+    const int h = e / DH;
+    float v = 0.0f;
+    for (int k = 0; k < ctas; ++k)
+      if (has(k)) v = fmaf(args.part_o[(slot0 + k * args.heads) * DH + e], ex2(args.part_ml[slot0 + k * args.heads + h].x - f[h].x), v);
+    st_from_float(static_cast<T*>(a.o) + b * a.o_ld + (static_cast<int64_t>(hk) * group + args.h0) * DH + e, v * f[h].y);
+  }
+  if (!args.x) return;
+  for (int i0 = blockIdx.x * kFinishKeys + tid; i0 < n; i0 += blocks * kFinishKeys) {
+    float* weight = c.weight + pair * c.cap + i0;
+    const float* x = args.x + pair * args.heads * args.x_ld + i0;
+    float w0[4], v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      w0[u] = i0 + u * kThreads < n ? weight[u * kThreads] : 0.0f;
+      v[u] = 0.0f;
+    }
+#pragma unroll 4
+    for (int h = 0; h < heads; ++h) {
+      const float2 fh = f[h];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kThreads < n) v[u] = fmaf(ex2(x[h * args.x_ld + u * kThreads] - fh.x), fh.y, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * kThreads < n) weight[u * kThreads] = w0[u] + v[u];
+  }
+}
+
 int32_t validate(const spatten_kv4_attn_args& a) {
   SPT_TRY(kv4_validate(a.cache));
   if (a.H < 1 || a.H > 1024) return SPATTEN_E_ARG;
@@ -660,51 +883,72 @@ int32_t validate(const spatten_kv4_attn_args& a) {
 
 struct Shape {
   int C;           // CTAs per (sequence, key/value head)
-  int x_ld, heads;
+  int64_t x_ld;
+  int heads;
   size_t x_smem;   // bytes of scores in shared memory (0: none, or in the workspace)
-  bool x_ws;
+  bool x_ws, split;
+  int ctas;        // of the split form
 };
 
-// Enough CTAs to fill the SMs, none with less than a tile per warp, and scores that let two CTAs share
-// an SM where more CTAs achieve that; scores that fit no SM go to the workspace.
-// (an SM has 228 KB, 1 KB of it per CTA reserved; a CTA's static arrays take up to 16 KB where two fit, else 20)
-constexpr size_t kSharedTwo = (113 - 16) * 1024, kSharedOne = (227 - 20) * 1024;   // ring and scores
+// ring and scores (an SM has 228 KB, 1 KB of it per CTA reserved; a CTA's static arrays take up to 16 KB where two
+// fit, else 20)
+constexpr size_t kSharedTwo = (113 - 16) * 1024, kSharedOne = (227 - 20) * 1024;
 
+// One launch of clusters: enough CTAs to fill the SMs, none with less than a tile per warp, and scores that let two
+// CTAs share an SM where more CTAs achieve that.  What takes more than one wave of them, or has scores that fit no
+// SM, is split instead (32 x 16384 rows, 8 heads of 128 with 4 queries each: <T_SPLIT> against 174 us; batches of
+// more than 1024 sequences, through which every CTA would have to look, are not).
 Shape shape(const spatten_kv4_attn_args& a) {
   Shape s{};
   const int tk = 2048 / a.cache.d_h;
   s.heads = std::min(a.H / a.cache.H_kv, kMaxHeads);
   const int64_t pairs = static_cast<int64_t>(a.cache.B) * a.cache.H_kv;
-  auto ld = [&](int C) { return static_cast<int>(align_up(static_cast<size_t>(ceil_div(a.n_max, C)), 32) + 4); };
+  auto ld = [&](int C) { return static_cast<int64_t>(align_up(static_cast<size_t>(ceil_div(a.n_max, C)), 32) + 4); };
   const size_t ring = ring_bytes(a.cache.d_h, s.heads > 8 ? 2 : 1);
   auto bytes = [&](int C) { return ring + (a.update_weight ? static_cast<size_t>(s.heads) * ld(C) * sizeof(float) : 0); };
   s.C = 1;
   while (s.C < kMaxC && a.n_max > s.C * kWarps * tk && (pairs * s.C < sm_count() || bytes(s.C) > kSharedTwo)) s.C *= 2;
-  s.x_ld = ld(s.C);
   s.x_ws = bytes(s.C) > kSharedOne;
-  s.x_smem = s.x_ws ? 0 : bytes(s.C) - ring;
+  const int per_sm = s.heads > 8 && a.dtype == SPATTEN_F32 ? 1 : 2;
+  s.ctas = per_sm * sm_count();
+  s.split = (pairs * s.C > s.ctas || s.x_ws) && a.cache.B <= 1024 && a.n_max > kWarps * tk;
+  if (s.split) s.C = 1;
+  s.x_ld = ld(s.C);
+  s.x_smem = s.x_ws || s.split ? 0 : bytes(s.C) - ring;
   return s;
 }
 
 size_t layout(const spatten_kv4_attn_args& a, void* ws, size_t ws_bytes, AttnArgs* x) {
   const Shape s = shape(a);
   WsCursor c(ws, ws_bytes);
-  float* p = s.x_ws ? c.take<float>(static_cast<size_t>(a.cache.B) * a.cache.H_kv * s.C * s.heads * s.x_ld) : nullptr;
-  if (x) x->x = p, x->x_ld = s.x_ld, x->heads = s.heads;
+  const size_t pairs = static_cast<size_t>(a.cache.B) * a.cache.H_kv, slots = pairs + s.ctas;
+  float* p = (s.x_ws || s.split) && a.update_weight ? c.take<float>(pairs * s.C * s.heads * s.x_ld) : nullptr;
+  float2* ml = s.split ? c.take<float2>(slots * s.heads) : nullptr;
+  float* o = s.split ? c.take<float>(slots * s.heads * a.cache.d_h) : nullptr;
+  if (x) x->x = p, x->x_ld = s.x_ld, x->heads = s.heads, x->ctas = s.ctas, x->part_ml = ml, x->part_o = o;
   return align_up(std::max<size_t>(c.used, 1), 256);   // never 0: callers allocate it as it comes
 }
 
 template <int DH, int NH, typename T>
-int32_t launch(const AttnArgs& x, const Shape& s, cudaStream_t st) {
+int32_t launch(AttnArgs x, const Shape& s, cudaStream_t st) {
   static DeviceOnce once;
   int dev;
   SPT_TRY(once_per_device(once, &dev, [](int) -> int32_t {
-    SPT_CUDA(cudaFuncSetAttribute(kv4_attn_kernel<DH, NH, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(kSharedOne)));
+    SPT_CUDA(cudaFuncSetAttribute(kv4_attn_kernel<DH, NH, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSharedOne)));
+    SPT_CUDA(cudaFuncSetAttribute(kv4_attn_split_kernel<DH, NH, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(DH, NH)));
     return SPATTEN_OK;
   }));
-  return launch_chained(kv4_attn_kernel<DH, NH, T>, dim3(s.C, x.a.cache.H_kv, x.a.cache.B), dim3(kThreads),
-                        ring_bytes(DH, NH) + s.x_smem, st, s.C, x);
+  const spatten_kv4_cache& c = x.a.cache;
+  if (!s.split)
+    return launch_chained(kv4_attn_kernel<DH, NH, T>, dim3(s.C, c.H_kv, c.B), dim3(kThreads), ring_bytes(DH, NH) + s.x_smem, st, s.C, x);
+  for (; x.h0 < x.a.H / c.H_kv; x.h0 += kMaxHeads) {
+    SPT_TRY(launch_chained(kv4_attn_split_kernel<DH, NH, T>, dim3(s.ctas), dim3(kThreads), ring_bytes(DH, NH), st, 1, x));
+    // about a wave of blocks: each looks its pair's CTAs up before it works through its keys
+    const int64_t most = ceil_div(8 * sm_count(), static_cast<int64_t>(c.B) * c.H_kv);
+    const dim3 grid(static_cast<unsigned>(std::min(ceil_div(x.a.n_max, kFinishKeys), most)), c.H_kv, c.B);
+    SPT_TRY(launch_chained(kv4_attn_finish_kernel<DH, T>, grid, dim3(kThreads), 0, st, 1, x));
+  }
+  return SPATTEN_OK;
 }
 
 template <int DH, typename T>

@@ -658,3 +658,30 @@ def test_calls_back_to_back_see_each_other(cuda):
 
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,d,B,Hk,H,cap,n", [
+    (BF, 64, 33, 16, 16, 300, [300, 0, 1] + [17 * i % 301 for i in range(30)]),     # many pairs, empty ones among them
+    (BF, 128, 40, 8, 32, 260, [1] * 39 + [260]),                                    # nearly all in one sequence
+    (F32, 64, 10, 32, 64, 280, [0] * 9 + [5]),                                      # fewer tiles than CTAs
+    (BF, 128, 80, 4, 96, 150, [150 - i for i in range(80)]),                        # more heads than one pass takes
+    (F32, 128, 75, 4, 4, 200, [200 - 2 * i for i in range(75)])])
+def test_attention_dealt_over_the_gpu(cuda, dtype, d, B, Hk, H, cap, n):
+    """More (sequence, head) pairs than one wave of CTAs: the keys are dealt in equal runs."""
+    S = lib()
+    c = Cache(S, B, Hk, d, cap, seed=B)
+    q = torch.randn((B, H, d), device="cuda").to(dtype)
+    w0 = c.t["weight"].clone()
+    o, status = run_attention(S, c, q, n)
+    assert status == 0
+    k, v = c.values()
+    got, got_w = host(o), host(c.t["weight"])
+    for b in list(range(0, B, 7)) + [B - 1, 1]:
+        ref, w = R.kv4_attention(host(q)[b], k[b], v[b], n[b])
+        spread, _ = R.kv4_attention(host(q)[b], k[b], np.abs(v[b]), n[b])
+        e = score_step(host(q)[b], k[b], n[b])
+        check_out(got[b], ref, spread, e, dtype, UBF if dtype == BF else 2 * U32, f"sequence {b}")
+        check_weight(got_w[b], host(w0)[b], w, e)
+        assert (got_w[b][:, n[b]:] == host(w0)[b][:, n[b]:]).all()
+    o2, _ = run_attention(S, c, q, n, update=False)
+    assert torch.equal(o, o2)
