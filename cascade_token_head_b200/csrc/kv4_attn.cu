@@ -8,7 +8,9 @@
 //            low bits of a half is the subnormal u 2^-24, one place higher 16 u 2^-24: no conversion
 //            beyond the masks; the 16 is taken out of q, and the 8 enters as the accumulator's start,
 //            -8 sum(q).  q is scaled by a power of two to a maximum in [2^13, 2^14) and rounded to fp16
-//            (bfloat16 queries: exact down to 2^-27 of the maximum), float32 queries as the sum of two.
+//            (bfloat16 queries: exact down to 2^-27 of the maximum).  Float32 queries are the sum of two
+//            fp16, and against them the nibbles become codes, 1024 + u - 1032: the sums with u in place of
+//            the code are larger and cost two bits.
 //   output   O^T[16 channels][8 heads] += codes . P', P' = exp(S - m) times the key's scale of the
 //            group, rounded to bfloat16 (its range is that of the scales) for bfloat16 queries and
 //            held as the sum of three bfloat16 (24 bits) for float32 ones; movmatrix turns P' from the
@@ -128,6 +130,16 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   return r;
 }
 
+// two nibbles at bits 0-3 and 16-19 (ODD: 4-7 and 20-23) of w as the fp16 pair of their codes, exact
+template <bool ODD>
+__device__ __forceinline__ uint32_t code_pair_f16(uint32_t w) {
+  const uint32_t u = (w & (ODD ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;   // 1024 + u, 1024 + 16 u
+  uint32_t r;
+  if constexpr (ODD) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x2c002c00u), "r"(0xd480d480u));   // / 16 - 72
+  else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0xe408e408u));                                   // - 1032
+  return r;
+}
+
 // Where row r of a tile of V codes lies in its stage: with the rows of a quad's four lanes (2t, or
 // 2t + 1) in neighbouring slots, and at 128 channels 32 bytes apart in every other pair of slots, a warp's
 // reads of V take every bank once.
@@ -205,7 +217,7 @@ struct Warp {
     uint32_t u[kQ][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {   // channels c, c + 4 of the word; the odd ones against 16 u
-      const float w = (c & 1) ? 0.0625f : 1.0f;
+      const float w = !kF32 && (c & 1) ? 0.0625f : 1.0f;
       float x = g[c] * up * w, y = g[c + 4] * up * w;
 #pragma unroll
       for (int e = 0; e < kQ; ++e) {
@@ -290,7 +302,12 @@ struct Warp {
       }
     }
     float s[NH][4];
-    {
+    if constexpr (kF32) {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[nh][k] = 0.0f;
+    } else {
       // 128 channels: scales 0, 1 on even, 2, 3 on odd lanes of a quad
       const uint8_t* sa = DH == 128 ? ss + (t & 1) * 4 : ss;
       const uint32_t k0 = *reinterpret_cast<const uint32_t*>(sa), k1 = *reinterpret_cast<const uint32_t*>(sa + (DH == 128 ? 64 : 32));
@@ -301,8 +318,12 @@ struct Warp {
 #pragma unroll
     for (int j = 0; j < G32; ++j) {
       const uint32_t w0 = kw[0][j], w1 = kw[1][j], v0 = w0 >> 8, v1 = w1 >> 8;
-      const uint32_t a0[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
-      const uint32_t a1[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
+      uint32_t a0[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
+      uint32_t a1[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
+      if constexpr (kF32) {
+        a0[0] = code_pair_f16<false>(w0), a0[1] = code_pair_f16<false>(w1), a0[2] = code_pair_f16<true>(w0), a0[3] = code_pair_f16<true>(w1);
+        a1[0] = code_pair_f16<false>(v0), a1[1] = code_pair_f16<false>(v1), a1[2] = code_pair_f16<true>(v0), a1[3] = code_pair_f16<true>(v1);
+      }
       const float f0 = (j & 1) ? bf_hi(ks[0][j >> 1]) : bf_lo(ks[0][j >> 1]);
       const float f1 = (j & 1) ? bf_hi(ks[1][j >> 1]) : bf_lo(ks[1][j >> 1]);
 #pragma unroll
@@ -323,7 +344,8 @@ struct Warp {
     for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        s[nh][k] = (s[nh][k] * 4096.0f) * scale[nh][k & 1];   // 2^24 in two factors that stay in range
+        // 2^24 (of nibbles), 1 (of codes) 2^-E in two factors that stay in range
+        s[nh][k] = (s[nh][k] * (kF32 ? 1.0f / 4096.0f : 4096.0f)) * scale[nh][k & 1];
         if (!FULL && left <= (k < 2 ? 0 : 8)) s[nh][k] = -INFINITY;
         grown |= s[nh][k] > lim[nh][k & 1];
       }

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           if (t >= T[g]) continue;
           if (!wait(&bars.p_ready[g], t & 1)) break;
           tc_after_sync();
-          mma_pv<DH, KT, PL>(tmem + C::tO + g * DH, tmem + C::tS + g * C::kScores, dVt, t > 0 ? 1u : 0u);
+          mma_pv<DH, KT, PL>(tmem + C::tO + g * DH, tmem + C::tS + g * C::kScores, dVt, PL == 1 && t > 0 ? 1u : 0u);
           if (t + 1 < T[g]) {
             mma_scores<DH, KT, PL>(tmem + C::tS + g * C::kScores, dQ + g * (C::kQTile >> 4), dKt);   // over the P that the MMAs before it read
             commit_one(&bars.s_full[g]);
@@ -396,9 +396,26 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     const float c = a.sm_scale * kLog2e;
     const float2 cc = make_float2(c, c);
     float m = -INFINITY, l = 0.0f;   // maximum (log2 units) that P is relative to, sum of this half
+    // Float32: the tensor cores cut their sums off, so an output accumulated there over hundreds of steps drifts
+    // towards 0 by their number times 2^-25.  Each tile's P V (of which the small products come first) starts
+    // from 0 instead, and the tiles add up here, rounded to nearest.
+    float acc[PL == 3 ? DH : 1];
+#pragma unroll
+    for (int j = 0; j < (PL == 3 ? DH : 1); ++j) acc[j] = 0.0f;
+    auto add_tile = [&]() {
+#pragma unroll
+      for (int ch = 0; ch < (PL == 3 ? DH : 0); ch += 32) {
+        float o[32];
+        tmem_ld32(tO + ch, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[PL == 3 ? ch + j : 0] += o[j];
+      }
+    };
     for (int t = 0; t < my_T; ++t) {
       const bool ok = warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim);
       tc_after_sync();
+      if (PL == 3 && ok && t > 0) add_tile();   // the score MMA was issued behind the previous P V
       const int j0 = t * KT + half * 64, lim = last - j0;   // columns 0 .. lim are seen
       const bool full = last_first - j0 >= 63;              // by every row of the warp
       float mx = -INFINITY;
@@ -449,7 +466,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         m = mn;
         l *= f;
         // the score MMA of this tile was issued behind the previous P V, so O is complete here
-        if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+        if constexpr (PL == 3) {
+#pragma unroll
+          for (int j = 0; j < DH; ++j) acc[j] *= f;
+        } else if (t > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
           for (int ch = 0; ch < kOCols; ch += 32) {
             float o[32];
@@ -550,29 +570,30 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       tc_after_sync();
       const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
       using T = std::conditional_t<PL == 1, __nv_bfloat16, float>;
+      if (PL == 3 && my_T > 0) add_tile();
       uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
+      if constexpr (PL == 3) {
+        if (r < my_rows)
+#pragma unroll
+          for (int j = 0; j < DH; j += 4)
+            dst[j / 4] = make_uint4(__float_as_uint(acc[j] * inv), __float_as_uint(acc[j + 1] * inv), __float_as_uint(acc[j + 2] * inv),
+                                    __float_as_uint(acc[j + 3] * inv));
+      } else {
 #pragma unroll 1
-      for (int ch = 0; ch < kOCols / 32; ++ch) {
-        float o[32];
-        if (my_T > 0) {
-          tmem_ld32(tO + ch * 32, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-        }
-        if (r < my_rows) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] *= inv;
-          if constexpr (PL == 1) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                                           pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+        for (int ch = 0; ch < kOCols / 32; ++ch) {
+          float o[32];
+          if (my_T > 0) {
+            tmem_ld32(tO + ch * 32, o);
+            tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[ch * 8 + q] = make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]), __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3]));
+            for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+          }
+          if (r < my_rows) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                           pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
           }
         }
       }
