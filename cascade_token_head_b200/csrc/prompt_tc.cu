@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
 // =================================================================================================
 // WEIGHT
 // =================================================================================================
-template <int DH_, int STAGES, int PL_ = 1>
+template <int DH_, int STAGES, int BUFS_, int CTAS, int PL_ = 1>
 struct WeightCfg {
   static constexpr int DH = DH_, PL = PL_;
   static constexpr int kStages = STAGES;
@@ -621,8 +621,9 @@ struct WeightCfg {
   static constexpr uint32_t oQ = kTile + kExtra, kStage = kTile + kExtra;
   static constexpr uint32_t kSmem = oQ + kStages * kStage + 1024u;
   static constexpr int kSoftmax = 256, kThreads = kSoftmax + 64;
-  static constexpr uint32_t kTmem = 256;   // two score buffers
-  static constexpr int kCtas = 2 * kSmem > 226 * 1024 ? 1 : 2;
+  static constexpr int kBufs = BUFS_, kCtas = CTAS;   // score buffers; CTAs per SM
+  static constexpr uint32_t kTmem = 128 * kBufs;
+  static_assert(CTAS * (kSmem + 2048) <= 228 * 1024 && CTAS * kTmem <= 512, "CTAs per SM");
 };
 
 // The row's offset -(m + log2 l) / c enters the scores by an MMA step of 16 channels more: the keys' are three
@@ -648,7 +649,7 @@ struct WeightBars {
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
-  constexpr int DH = C::DH, PL = C::PL, NST = C::kStages;
+  constexpr int DH = C::DH, PL = C::PL, NST = C::kStages, NB = C::kBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ WeightBars<NST> bars;
@@ -765,14 +766,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
       for (int t = 0; t < NT && !aborted; ++t) {
         const int s = t % NST;
         if (!warp_wait(&bars.q_full[s], (t / NST) & 1, abort_flag, wlim) ||
-            !warp_wait(&bars.s_empty[t & 1], ((t >> 1) & 1) ^ 1u, abort_flag, wlim)) {
+            !warp_wait(&bars.s_empty[t % NB], ((t / NB) & 1) ^ 1u, abort_flag, wlim)) {
           aborted = true;
           break;
         }
         tc_after_sync();
-        mma_scores<DH, kRows, PL>(tmem + (t & 1) * 128, dK, dQ + s * (C::kStage >> 4));
-        if (elect_one()) mma_f16(tmem + (t & 1) * 128, eK, eQ + s * (C::kStage >> 4), id, 1u);
-        commit_one(&bars.s_full[t & 1]);
+        mma_scores<DH, kRows, PL>(tmem + (t % NB) * 128, dK, dQ + s * (C::kStage >> 4));
+        if (elect_one()) mma_f16(tmem + (t % NB) * 128, eK, eQ + s * (C::kStage >> 4), id, 1u);
+        commit_one(&bars.s_full[t % NB]);
         commit_one(&bars.q_empty[s]);
       }
       if (aborted) {
@@ -789,31 +790,35 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
     const float2 cc = make_float2(c, c);
     for (int t = 0; t < NT; ++t) {
       const int i0 = (rt0 + t) * kRows;
-      if (!warp_wait(&bars.s_full[t & 1], (t >> 1) & 1, abort_flag, wlim)) {
+      if (!warp_wait(&bars.s_full[t % NB], (t / NB) & 1, abort_flag, wlim)) {
         aborted = true;
         break;
       }
       tc_after_sync();
-      const uint32_t tS = tmem + lanes + (t & 1) * 128 + col0;
+      const uint32_t tS = tmem + lanes + (t % NB) * 128 + col0;
       const int lo = j - shift - i0 - col0, hi = qr.n - i0 - col0;   // columns lo .. hi - 1 see the key
       const int lo_first = lo - lane;                                // the same for the warp's first key
       float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
       if (lo_first + 31 <= 0 && hi >= 64) {   // all of the warp's
-        float v[64];
-        tmem_ld32(tS, v);
-        tmem_ld32(tS + 32, v + 32);
-        tmem_ld_wait();
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
 #pragma unroll
-        for (int q = 0; q < 64; q += 8) {
-          const float2 e0 = exp2_pair<0, kWeightPoly>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
-          const float2 e1 = exp2_pair<1, kWeightPoly>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
-          const float2 e2 = exp2_pair<2, kWeightPoly>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
-          const float2 e3 = exp2_pair<3, kWeightPoly>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
-          s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
-          s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
+        for (int ch = 0; ch < 2; ++ch) {   // 32 at a time: registers for three CTAs
+          float v[32];
+          tmem_ld32(tS + ch * 32, v);
+          tmem_ld_wait();
+          if (ch == 1) {
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_empty[t % NB]);
+          }
+#pragma unroll
+          for (int q = 0; q < 32; q += 8) {
+            const float2 e0 = exp2_pair<0, kWeightPoly>(__fmul2_rn(make_float2(v[q], v[q + 1]), cc));
+            const float2 e1 = exp2_pair<1, kWeightPoly>(__fmul2_rn(make_float2(v[q + 2], v[q + 3]), cc));
+            const float2 e2 = exp2_pair<2, kWeightPoly>(__fmul2_rn(make_float2(v[q + 4], v[q + 5]), cc));
+            const float2 e3 = exp2_pair<3, kWeightPoly>(__fmul2_rn(make_float2(v[q + 6], v[q + 7]), cc));
+            s0 = __fadd2_rn(s0, __fadd2_rn(e0, e2));
+            s1 = __fadd2_rn(s1, __fadd2_rn(e1, e3));
+          }
         }
       } else {
 #pragma unroll 1
@@ -831,7 +836,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
         }
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.s_empty[t & 1]);
+        if (lane == 0) mbar_arrive(&bars.s_empty[t % NB]);
       }
       total += (s0.x + s1.x) + (s0.y + s1.y);
     }
@@ -966,9 +971,9 @@ bool prompt_tc_supported(const spatten_prompt_args& a) {
 
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st) {
   if (p.a.dtype == SPATTEN_BF16)
-    return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 4>, WeightCfg<64, 3>>(p, st) : launch<OutCfg<128, 2, 128, 4>, WeightCfg<128, 2>>(p, st);
-  return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 2, 3>, WeightCfg<64, 1, 3>>(p, st)
-                       : launch<OutCfg<128, 1, 64, 2, 3>, WeightCfg<128, 1, 3>>(p, st);
+    return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 4>, WeightCfg<64, 2, 1, 3>>(p, st) : launch<OutCfg<128, 2, 128, 4>, WeightCfg<128, 1, 1, 3>>(p, st);
+  return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 2, 3>, WeightCfg<64, 1, 2, 2, 3>>(p, st)
+                       : launch<OutCfg<128, 1, 64, 2, 3>, WeightCfg<128, 1, 2, 1, 3>>(p, st);
 }
 
 }  // namespace spt
