@@ -2,6 +2,8 @@
 // rows with the least attention weight).  Layout and rules: spatten.h.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace cg = cooperative_groups;
@@ -169,28 +171,15 @@ __device__ __forceinline__ int v_word_at(int oct) {
   return run * (DH / 64) + (g >> 1);
 }
 
-// Stores eight quantized channels of cache row `at` (over all heads and rows); whole warps call it, `ok`
-// says whether this lane has a row.
-template <int DH, typename X>
-__device__ __forceinline__ void append8(const AppendArgs& a, int tensor, const X& x, int64_t at, int oct, bool ok) {
-  constexpr int G = DH / kKv4Group;
-  uint32_t sb;
-  bool bad;
-  uint32_t w = quantize8(x, &sb, &bad);
-  if (tensor) w = v_word<DH>(w, oct);
-  if (!ok) return;
-  if (bad) report(a.status, SPATTEN_E_NONFINITE);
-  reinterpret_cast<uint32_t*>(tensor ? a.c.v_codes : a.c.k_codes)[at * (DH / 8) + (tensor ? v_word_at<DH>(oct) : k_word_at<DH>(oct))] = w;
-  if ((oct & 3) == 0) (tensor ? a.c.v_scale : a.c.k_scale)[at * G + (oct >> 2)] = static_cast<uint16_t>(sb);
-}
-
-// Packed rows: a warp takes kSteps * 256 / DH rows of one head, eight channels a lane and step, all loads
-// before the first use: rows of a head are whole lines on both sides.  Bound by memory and, next to it, by
-// the quantization's instructions: 16,384 rows of 16 heads of 64 (bfloat16, 86 MB) take <T_APPEND>.
+// Packed rows: a warp takes runs of kSteps * 256 / DH rows of one head, eight channels a lane and step, all
+// loads before the first use: rows of a head are whole lines on both sides.  Bound by the quantization's
+// instructions and, next to them, by memory: <T_APPEND>
 template <int DH> constexpr int kRowLanes = DH / 8;
 constexpr int kSteps = 4;
-template <int DH> constexpr int kTaskRows = kSteps * 32 / kRowLanes<DH>;
-template <int DH> constexpr int kBlockRows = kTaskRows<DH> * (kThreads / 32);   // of one sequence
+constexpr int kChunks = 2, kReadChunks = 1;   // runs a warp: blocks that look their rows up, against blocks to even out
+template <int DH> constexpr int kStepRows = 32 / kRowLanes<DH>;
+template <int DH> constexpr int kTaskRows = kSteps * kStepRows<DH>;
+template <int DH, int CHUNKS> constexpr int kBlockRows = CHUNKS * kTaskRows<DH> * (kThreads / 32);   // of one sequence
 
 // The rows i0 .. of sequence b (n rows from packed row `first`) that block blockIdx.x works on; b = -1: none.
 // The whole block calls it, once.
@@ -223,35 +212,56 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, b
       if (a.seen_out) a.seen_out[s] = a.seen[s] + n;
     }
   const int h = blockIdx.y;
-  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH>);
-  const int i0 = p.i0 + (threadIdx.x >> 5) * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);   // rows of the warp
-  if (p.b < 0 || n <= 0) return;
-  const int old = clamp_len(a.len[p.b], a.c.cap, a.status);
-  const int room = a.c.cap - old - i0;   // of which these fit
-  if (room < n && lane == 0) report(a.status, SPATTEN_E_INDEX);
-  const int fit = min(n, room);
-  if (fit <= 0) return;
-  const int64_t src = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
-  const int64_t row0 = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap + old + i0;
+  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH, kChunks>);
+  if (p.b < 0) return;
+  constexpr int G = DH / kKv4Group;
+  const int old = clamp_len(a.len[p.b], a.c.cap, a.status), r = lane / kRowLanes<DH>;
+  const int64_t pair = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap;
+  bool bad = false;
+#pragma unroll 1
+  for (int c = 0; c < kChunks; ++c) {
+    const int i0 = p.i0 + (c * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * kTaskRows<DH>;
+    const int n = min(kTaskRows<DH>, p.n - i0);   // rows of the run
+    const int room = a.c.cap - old - i0;          // of which these fit
+    if (n > 0 && room < n && lane == 0) report(a.status, SPATTEN_E_INDEX);
+    const int fit = min(n, room);
+    if (fit <= 0) break;   // as for the runs behind
+    const int64_t row0 = pair + old + i0, src = (static_cast<int64_t>(p.first) + i0 + r) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
+    auto run = [&](auto full, int t) {   // full: all rows of the run are there
+      constexpr bool kFull = decltype(full)::value;
+      const T* x = static_cast<const T*>(t ? a.x[1] : a.x[0]) + src;
+      uint32_t* codes = reinterpret_cast<uint32_t*>(t ? a.c.v_codes : a.c.k_codes) + (row0 + r) * (DH / 8) + (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct));
+      uint16_t* scale = (t ? a.c.v_scale : a.c.k_scale) + (row0 + r) * G + (oct >> 2);
+      typename Octet<T>::type v[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        if (kFull || k * kStepRows<DH> + r < fit) v[k].load(x + k * kStepRows<DH> * a.ld_tok);
+        else v[k].zero();
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t sb;
+        bool nonfinite;
+        uint32_t w = quantize8(v[k], &sb, &nonfinite);
+        if (t) w = v_word<DH>(w, oct);
+        bad |= nonfinite;
+        if (kFull || k * kStepRows<DH> + r < fit) {
+          codes[k * kStepRows<DH> * (DH / 8)] = w;
+          if ((oct & 3) == 0) scale[k * kStepRows<DH> * G] = static_cast<uint16_t>(sb);
+        }
+      }
+    };
 #pragma unroll 1   // unrolled it is too large for the instruction cache
-  for (int t = 0; t < 2; ++t) {
-    typename Octet<T>::type x[kSteps];
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      if (r < fit) x[k].load(static_cast<const T*>(t ? a.x[1] : a.x[0]) + src + r * a.ld_tok);
-      else x[k].zero();
+    for (int t = 0; t < 2; ++t) {
+      if (fit == kTaskRows<DH>) run(std::true_type{}, t);
+      else run(std::false_type{}, t);
     }
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      append8<DH>(a, t, x[k], row0 + r, oct, r < fit);
+    if (lane < fit) {
+      if (a.c.weight) a.c.weight[row0 + lane] = 0.0f;
+      if (a.c.pos) a.c.pos[row0 + lane] = a.seen[p.b] + i0 + lane;
     }
   }
-  if (lane < fit) {
-    if (a.c.weight) a.c.weight[row0 + lane] = 0.0f;
-    if (a.c.pos) a.c.pos[row0 + lane] = a.seen[p.b] + i0 + lane;
-  }
+  if (bad) report(a.status, SPATTEN_E_NONFINITE);
 }
 
 // The counts of a call whose outputs are its inputs, after the rows.
@@ -318,7 +328,7 @@ int32_t append_launch(const AppendArgs& a, cudaStream_t st) {
   const bool apart = a.len_out != a.len && (!a.seen_out || a.seen_out != a.seen);
   if (a.total > 0) {
     // a sequence's rows end in at most one partial run, so this many cover any offsets
-    const dim3 grid(a.total / kBlockRows<DH> + a.c.B, a.c.H_kv);
+    const dim3 grid(a.total / kBlockRows<DH, kChunks> + a.c.B, a.c.H_kv);
     SPT_TRY(launch_chained(kv4_append_kernel<DH, T>, grid, dim3(kThreads), 0, st, 1, a, apart));
     if (apart) return SPATTEN_OK;
   }
@@ -364,7 +374,7 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint3
 // A warp takes the rows of one head as the append kernel does, all loads before the first use.  Bound by
 // memory: 16,384 rows of 16 heads of 64 to bfloat16 (86 MB) take <T_READ>.
 template <int DH, typename T>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(ReadArgs a) {
   grid_dep_trigger();
   grid_dep_wait();
   constexpr int G = DH / kKv4Group;
@@ -373,34 +383,51 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ReadArgs a) {
     for (int b = threadIdx.x; b < a.c.B; b += kThreads)
       if (packed_rows(a.cu, b, a.total).bad) report(a.status, SPATTEN_E_INDEX);
   const int h = blockIdx.y;
-  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH>);
-  const int i0 = p.i0 + (threadIdx.x >> 5) * kTaskRows<DH>, n = min(kTaskRows<DH>, p.n - i0);
-  if (p.b < 0 || n <= 0) return;
-  const int64_t first = static_cast<int64_t>(a.row0 ? a.row0[p.b] : 0) + i0;   // cache row of the task's first
-  if (lane == 0 && (first < 0 || first + n > a.c.cap)) report(a.status, SPATTEN_E_INDEX);
-  const int64_t base = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap + first;
-  const int64_t dst = (static_cast<int64_t>(p.first) + i0) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
-  uint32_t w[2][kSteps];
-  uint32_t s[2][kSteps];
+  const BlockRows p = find_block_rows(a.cu, a.c.B, a.total, kBlockRows<DH, kReadChunks>);
+  if (p.b < 0) return;
+  const int row0 = a.row0 ? a.row0[p.b] : 0, r = lane / kRowLanes<DH>;
+  const int64_t pair = (static_cast<int64_t>(p.b) * a.c.H_kv + h) * a.c.cap;
+#pragma unroll 1
+  for (int c = 0; c < kReadChunks; ++c) {
+    const int i0 = p.i0 + (c * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * kTaskRows<DH>;
+    const int n = min(kTaskRows<DH>, p.n - i0);
+    if (n <= 0) break;
+    const int64_t first = static_cast<int64_t>(row0) + i0;   // cache row of the run's first
+    const bool inside = first >= 0 && first + n <= a.c.cap;
+    if (lane == 0 && !inside) report(a.status, SPATTEN_E_INDEX);
+    const int64_t dst = (static_cast<int64_t>(p.first) + i0 + r) * a.ld_tok + static_cast<int64_t>(h) * DH + oct * 8;
+    auto run = [&](auto full) {   // full: all rows of the run are there; else rows outside the cache read as 0
+      constexpr bool kFull = decltype(full)::value;
+      const int lo = first < -kTaskRows<DH> ? kTaskRows<DH> : max(0, -static_cast<int>(first));
+      const int hi = first + n <= a.c.cap ? n : (first < a.c.cap ? static_cast<int>(a.c.cap - first) : 0);
+      uint32_t w[2][kSteps], s[2][kSteps];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(t ? a.c.v_codes : a.c.k_codes) + (pair + first + r) * (DH / 8) +
+                                (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct));
+        const uint16_t* scale = (t ? a.c.v_scale : a.c.k_scale) + (pair + first + r) * G + g;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      const bool ok = r < n && first + r >= 0 && first + r < a.c.cap && a.out[t];   // else 0
-      w[t][k] = ok ? reinterpret_cast<const uint32_t*>(t ? a.c.v_codes : a.c.k_codes)[(base + r) * (DH / 8) + (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct))] : 0u;
-      s[t][k] = ok ? (t ? a.c.v_scale : a.c.k_scale)[(base + r) * G + g] : 0u;
-    }
+        for (int k = 0; k < kSteps; ++k) {
+          const int i = k * kStepRows<DH> + r;
+          const bool ok = kFull || (i >= lo && i < hi);
+          w[t][k] = ok ? codes[k * kStepRows<DH> * (DH / 8)] : 0u;
+          s[t][k] = ok ? scale[k * kStepRows<DH> * G] : 0u;
+        }
+      }
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    T* out = static_cast<T*>(a.out[t]);
-    if (!out) continue;
+      for (int t = 0; t < 2; ++t) {
+        T* out = static_cast<T*>(a.out[t]);
+        if (!out) continue;
+        out += dst;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int r = k * (32 / kRowLanes<DH>) + lane / kRowLanes<DH>;
-      const uint32_t u = t ? v_word<DH>(w[t][k], oct) : w[t][k];
-      if (r < n) store_values(out + dst + r * a.ld_tok, u, s[t][k]);
-    }
+        for (int k = 0; k < kSteps; ++k) {
+          const uint32_t u = t ? v_word<DH>(w[t][k], oct) : w[t][k];
+          if (kFull || k * kStepRows<DH> + r < n) store_values(out + k * kStepRows<DH> * a.ld_tok, u, s[t][k]);
+        }
+      }
+    };
+    if (inside && n == kTaskRows<DH>) run(std::true_type{});
+    else run(std::false_type{});
   }
 }
 
@@ -937,7 +964,7 @@ extern "C" int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* c
   if (!aligned16(k_out) || !aligned16(v_out) || (ld_tok * esz) % 16 != 0) return SPATTEN_E_ALIGN;
   if (total == 0) return SPATTEN_OK;
   const ReadArgs a{*c, cu, row0, total, {k_out, v_out}, ld_tok, dev_status};
-  const dim3 grid(total / (c->d_h == 64 ? kBlockRows<64> : kBlockRows<128>) + c->B, c->H_kv);
+  const dim3 grid(total / (c->d_h == 64 ? kBlockRows<64, kReadChunks> : kBlockRows<128, kReadChunks>) + c->B, c->H_kv);
   const bool bf = dtype == SPATTEN_BF16;
   const auto kernel = c->d_h == 64 ? (bf ? kv4_read_kernel<64, __nv_bfloat16> : kv4_read_kernel<64, float>)
                                    : (bf ? kv4_read_kernel<128, __nv_bfloat16> : kv4_read_kernel<128, float>);
