@@ -932,7 +932,7 @@ extern "C" int32_t spatten_kv4_append(const spatten_kv4_cache* c, const void* k,
                                       int32_t* dev_status, void* stream) {
   spt::AbiRange nvtx_range("spatten_kv4_append");
   using namespace spt;
-  if (!c || !k || !v || !len || !len_out) return SPATTEN_E_ARG;
+  if (!c || (total != 0 && (!k || !v)) || !len || !len_out) return SPATTEN_E_ARG;
   SPT_TRY(kv4_validate(*c));
   if (dtype != SPATTEN_F32 && dtype != SPATTEN_BF16) return SPATTEN_E_ARG;
   if (total < 0) return SPATTEN_E_ARG;
@@ -955,7 +955,7 @@ extern "C" int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* c
                                     void* stream) {
   spt::AbiRange nvtx_range("spatten_kv4_read");
   using namespace spt;
-  if (!c || !cu || (!k_out && !v_out)) return SPATTEN_E_ARG;
+  if (!c || !cu || (total != 0 && !k_out && !v_out)) return SPATTEN_E_ARG;
   SPT_TRY(kv4_validate(*c));
   if (dtype != SPATTEN_F32 && dtype != SPATTEN_BF16) return SPATTEN_E_ARG;
   if (total < 0) return SPATTEN_E_ARG;

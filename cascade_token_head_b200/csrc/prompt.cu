@@ -19,7 +19,7 @@ int32_t validate(const spatten_prompt_args& a) {
     return SPATTEN_E_ARG;
   if (a.d_h != 64 && a.d_h != 128) return SPATTEN_E_UNSUPPORTED;
   if (a.H % a.H_kv != 0) return SPATTEN_E_SHAPE;
-  if (!a.cu_q || !a.q || !a.k || !a.v || !a.o) return SPATTEN_E_ARG;
+  if (!a.cu_q || (a.total_q > 0 && (!a.q || !a.o)) || (a.total_kv > 0 && (!a.k || !a.v))) return SPATTEN_E_ARG;
   if (!a.cu_kv && a.total_q != a.total_kv) return SPATTEN_E_SHAPE;
   const int64_t hd = static_cast<int64_t>(a.H) * a.d_h, hkd = static_cast<int64_t>(a.H_kv) * a.d_h;
   if (a.q_ld_tok < hd || a.o_ld_tok < hd || a.kv_ld_tok < hkd) return SPATTEN_E_SHAPE;

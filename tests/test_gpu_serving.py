@@ -685,3 +685,82 @@ def test_attention_dealt_over_the_gpu(cuda, dtype, d, B, Hk, H, cap, n):
         assert (got_w[b][:, n[b]:] == host(w0)[b][:, n[b]:]).all()
     o2, _ = run_attention(S, c, q, n, update=False)
     assert torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64)])
+@pytest.mark.parametrize("B", [32, 33, 70])
+def test_prompt_many_sequences(cuda, dtype, d, B):
+    """More sequences than a warp has lanes, some without rows, some going on over earlier rows."""
+    r = np.random.default_rng(B + d)
+    lens = r.integers(0, 160, B)
+    lens[::7] = 0
+    old = r.integers(0, 2, B) * r.integers(0, 150, B)
+    Prompt(lib(), dtype, d, 2, 1, lens.tolist(), (lens + old).tolist(), seed=B).run().check(UBF if dtype == BF else 0.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_float32_on_cuda_cores(cuda, d):
+    Prompt(lib(), F32, d, 4, 2, [150, 0, 65], [150, 20, 200], seed=16, kernel=1).run().check(0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prompt_without_any_key(cuda, dtype):
+    """No sequence has keys: outputs of zero, weights as they were."""
+    Prompt(lib(), dtype, 64, 4, 2, [3, 70], [0, 0], seed=17).run().check(0.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_and_read_many_sequences(cuda, d):
+    """Prompts of 70 sequences (more than a warp has lanes) into the cache and back: the quantized rows."""
+    S, B, H = lib(), 70, 3
+    r = np.random.default_rng(d)
+    lens, old = r.integers(0, 40, B), r.integers(0, 9, B)
+    lens[3::9] = 0
+    c, cu = Cache(S, B, H, d, 50, seed=d), offsets(lens)
+    x = [torch.randn((cu[-1], H, d), device="cuda", generator=torch.Generator(device="cuda").manual_seed(d)) for _ in range(2)]
+    n, status = i32(old.tolist()), i32([0])
+    S.kv4_append(c.c, x[0], x[1], H * d, cu[-1], n, n, n.clone(), n.clone(), cu=i32(cu), dev_status=status)
+    out = [torch.empty_like(t) for t in x]
+    S.kv4_read(c.c, i32(cu), cu[-1], out[0], out[1], H * d, row0=i32(old.tolist()), dev_status=status)
+    assert n.tolist() == (old + lens).tolist() and int(status.item()) == 0
+    for t, o, run in ((x[0], out[0], 8), (x[1], out[1], 4)):
+        code, s = R.quantize4(t.cpu().numpy())
+        np.testing.assert_array_equal(host(o), code.astype(np.float64) * np.repeat(s, 32, axis=-1).astype(np.float64))
+
+
+def test_first_calls_are_captured(cuda):
+    """A process whose first calls of the library are inside a graph capture; replays give the eager bits."""
+    import os
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = """
+import torch
+from cascade_token_head_b200 import kv4
+def state():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = [torch.randn((90, h, 64), device="cuda", generator=g).to(torch.bfloat16) for h in (4, 2, 2)]
+    t = [torch.randn((2, h, 64), device="cuda", generator=g).to(torch.bfloat16) for h in (4, 2, 2)]
+    return kv4.KV4State(2, 4, 2, 64, 128), x, t, torch.empty_like(x[0]), torch.empty_like(t[0])
+cu = torch.tensor([0, 50, 90], dtype=torch.int32, device="cuda")
+def run(st, x, t, o, o1):
+    st.prompt(*x, cu, o)
+    st.evict(20, 4)
+    st.step(*t, o1)
+a, b = state(), state()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run(*a)
+g.replay()
+run(*b)
+torch.cuda.synchronize()
+for x, y in ((a[3], b[3]), (a[4], b[4]), (a[0].weight, b[0].weight), (a[0].k_codes, b[0].k_codes), (a[0].len, b[0].len)):
+    assert torch.equal(x, y)
+assert int(a[0].status) == int(b[0].status) == 0 and a[0].len.tolist() == [21, 21]
+print("same bits")
+"""
+    root = str(Path(__file__).resolve().parent.parent)
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, PYTHONPATH=root), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "same bits" in r.stdout, r.stdout + r.stderr
