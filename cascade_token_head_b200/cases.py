@@ -6,6 +6,8 @@
     python -m cascade_token_head_b200.cases decode_step --reps 4
     python -m cascade_token_head_b200.cases quantize --B 32 --H 12 --n 512 --d 64 --reps 3
     python -m cascade_token_head_b200.cases gather --B 32 --n 512 --k 461 --row-bytes 1536 --reps 3
+    python -m cascade_token_head_b200.cases prompt --B 16 --H 16 --H-kv 16 --n 512 --d 64 --reps 3
+    python -m cascade_token_head_b200.cases kv4_step --B 16 --H 16 --H-kv 16 --n 1152 --d 64 --reps 3
 
 Each prints one JSON line with the mean CUDA-event time per call and the algorithmic bytes or
 flops of one call.  Inputs are drawn on the host from a seeded generator and copied once.
@@ -171,11 +173,48 @@ def decode_step_case(reps, steps_done=0):
                 tokens_per_s=w.B / ms * 1e3)
 
 
+def prompt_case(B, H, H_kv, n, d, reps):
+    """Causal attention of B packed prompts of n tokens, with the weights an eviction needs."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rows = lambda h: torch.randn((B * n, h, d), generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = rows(H), rows(H_kv), rows(H_kv)
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    a = S.make_prompt_args(q, k, v, torch.empty_like(q), cu, weight=torch.zeros((B, H_kv, n), device="cuda"))
+    nb = S.prompt_workspace_size(a)
+    ws = torch.empty(max(nb, 1), dtype=torch.uint8, device="cuda")
+    ms = _time(lambda: S.prompt_attention(a, ws, nb), reps)
+    flops = 3.0 * B * H * n * (n + 1) * d   # scores twice and P V, half of the square each
+    return dict(case="prompt", B=B, H=H, H_kv=H_kv, n=n, d=d, ms=ms, flops=flops, tflops=flops / ms / 1e9)
+
+
+def kv4_step_case(B, H, H_kv, n, d, reps):
+    """A generated token of B sequences over the 4-bit cache at n rows: append, then attention."""
+    from .kv4 import KV4State
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rnd = lambda h: torch.randn((B, h, d), generator=g, device="cuda").to(torch.bfloat16)
+    st = KV4State(B, H, H_kv, d, n + 1)
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((B * n, H_kv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    st.append(k, v, cu)
+    q, k1, v1 = rnd(H), rnd(H_kv), rnd(H_kv)
+    o = torch.empty_like(q)
+
+    def step():   # the same token again: the row count is set back
+        st.len.fill_(n)
+        st.step(q, k1, v1, o)
+    ms = _time(step, reps)
+    assert int(st.status.item()) == 0
+    nbytes = B * H_kv * (n + 1) * (2 * (d // 2 + d // 16) + 8)
+    return dict(case="kv4_step", B=B, H=H, H_kv=H_kv, n=n, d=d, ms=ms, bytes=nbytes, gbs=nbytes / ms / 1e6)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["attention", "topk", "gather", "quantize", "decode", "decode_step"])
+    ap.add_argument("case", choices=["attention", "topk", "gather", "quantize", "decode", "decode_step", "prompt",
+                                     "kv4_step"])
     ap.add_argument("--B", type=int, default=32)
     ap.add_argument("--H", type=int, default=12)
+    ap.add_argument("--H-kv", type=int, default=12)
     ap.add_argument("--n", type=int, default=512)
     ap.add_argument("--d", type=int, default=64)
     ap.add_argument("--k", type=int, default=256)
@@ -198,6 +237,10 @@ def main(argv=None):
         r = quantize_case(a.B, a.H, a.n, a.d, a.reps)
     elif a.case == "decode":
         r = decode_case(a.B, a.H, a.n, a.d, a.keep, a.theta, a.reps, a.kernel)
+    elif a.case == "prompt":
+        r = prompt_case(a.B, a.H, a.H_kv, a.n, a.d, a.reps)
+    elif a.case == "kv4_step":
+        r = kv4_step_case(a.B, a.H, a.H_kv, a.n, a.d, a.reps)
     else:
         r = decode_step_case(a.reps)
     print(json.dumps(r), flush=True)
