@@ -42,6 +42,7 @@ struct AppendArgs {
 
 // Eight channels as they are loaded.
 struct Bf16x8 {
+  static constexpr bool kEightBits = true;   // significands
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
@@ -58,6 +59,7 @@ struct Bf16x8 {
   }
 };
 struct F32x8 {
+  static constexpr bool kEightBits = false;
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
@@ -107,16 +109,28 @@ __device__ __noinline__ uint2 quantize8_by_division(float4 a, float4 b) {
   return make_uint2(w, static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (bad ? 0x80000000u : 0u));
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Eight channels (one lane's share: a quarter of a 32-channel group) of one row to codes; the four
 // lanes of the group share their amax; whole warps call it.  Returns the codes as nibbles (channel i at
 // bits 4i) and the scale's bfloat16 bits.
-// Both roundings are those of IEEE quotients.  amax (1 / 7) is within 2 steps of the quotient, so both
-// round to the same bfloat16 unless it is that near to a border.  x / s is rounded as the quotient is by
-// Markstein's theorem (1990): with y = 1 / s rounded to nearest, q = x y and r = x - q s, which is exact,
-// q + r y rounds to the nearest x / s (s is no number of all ones: it has eight bits).  Borders, values
-// that are not finite and scales below 2^-100, where products underflow and the quotient may pass 7, make
-// the warp divide; elsewhere the quotient is at most 7 (1 + 2^-8).  Dividing everywhere took 1.7 times as
-// long (16,384 rows of 16 heads of 64).
+// Both roundings are those of IEEE quotients.
+//  float32   amax (1 / 7) is within 2 steps of the quotient, so both round to the same bfloat16 unless it
+//    is that near to a border.  x / s is rounded as the quotient is by Markstein's theorem (1990): with
+//    y = 1 / s rounded to nearest, q = x y and r = x - q s, which is exact, q + r y rounds to the nearest
+//    x / s (s is no number of all ones: it has eight bits).
+//  bfloat16  amax / 7 is never a border: that would have nine bits and its sevenfold more than eight; the
+//    next quotients are 2^-12 away.  x and s have eight bits, and x is at least s / 4 near a half, so
+//    |x / s - (k + 1/2)| = |2 x - (2 k + 1) s| / (2 s) is 0 or at least 1 / 1020.  x y (within 2^-19) rounded to
+//    multiples of 2^-12 is therefore the half itself or on the quotient's side of it, and the second rounding,
+//    to integers, is that of the quotient.
+// Borders, values that are not finite and scales below 2^-100, where products underflow and the quotient may
+// pass 7, make the warp divide; elsewhere the quotient is at most 7 (1 + 2^-8).  Dividing everywhere took 1.7
+// times as long (16,384 rows of 16 heads of 64).
 template <typename X>
 __device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits, bool* bad) {
   float x[8];
@@ -128,7 +142,7 @@ __device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits
   uint32_t sb = (q7 + 0x7fffu + ((q7 >> 16) & 1u)) >> 16;   // to the nearest bfloat16
   *bad = false;
   const bool zero = am == 0;
-  if (__any_sync(0xffffffffu, am >= 0x7f800000u || (q7 & 0xffffu) - 0x7ffcu <= 8u || (sb < (27u << 7) && !zero))) {
+  if (__any_sync(0xffffffffu, am >= 0x7f800000u || (!X::kEightBits && (q7 & 0xffffu) - 0x7ffcu <= 8u) || (sb < (27u << 7) && !zero))) {
     const uint2 r = quantize8_by_division(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]));
     *scale_bits = r.y & 0xffffu;
     *bad = r.y >> 31;
@@ -136,15 +150,23 @@ __device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits
   }
   sb = zero ? 0x3f80u : sb;
   *scale_bits = sb;
-  const float s = __uint_as_float(sb << 16), y = __frcp_rn(s);
+  const float s = __uint_as_float(sb << 16), y = X::kEightBits ? rcp_approx(s) : __frcp_rn(s);
   const float2 y2 = make_float2(y, y), s2 = make_float2(-s, -s);
-  constexpr float kCodeRound = 12582912.0f + 8.0f;   // 1.5 * 2^23 + 8: the sum's low bits are rint(x / s) + 8
-  const float2 up = make_float2(kCodeRound, kCodeRound);
+  constexpr float kCodeRound = 1.5f * 8388608.0f + 8.0f;   // 1.5 * 2^23 + 8: the sum's low bits are rint(x / s) + 8
+  constexpr float kFine = 1.5f * 2048.0f;                  // sums with it are multiples of 2^-12
+  const float2 up = make_float2(kCodeRound, kCodeRound), fine = make_float2(kFine, kFine);
+  const float2 rest = make_float2(kCodeRound - kFine, kCodeRound - kFine);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    const float2 v = make_float2(x[i], x[i + 1]), q = __fmul2_rn(v, y2);
-    const float2 t = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, s2, v), y2, q), up);
+    const float2 v = make_float2(x[i], x[i + 1]);
+    float2 t;
+    if constexpr (X::kEightBits) {
+      t = __fadd2_rn(__ffma2_rn(v, y2, fine), rest);
+    } else {
+      const float2 q = __fmul2_rn(v, y2);
+      t = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, s2, v), y2, q), up);
+    }
     // the sums' high bits are constants, which drop out at the end
     w += __float_as_uint(t.x) * (1u << (4 * i)) + __float_as_uint(t.y) * (16u << (4 * i));
   }
