@@ -83,8 +83,10 @@ template <> struct Octet<float> { using type = F32x8; };
 
 // What quantize8 does, by IEEE divisions: the codes, and the scale's bits with bit 31 set where this lane
 // held a value that is not finite.
-__device__ __noinline__ uint2 quantize8_by_division(float4 a, float4 b) {
-  float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+template <typename X>
+__device__ __noinline__ uint2 quantize8_by_division(X raw) {
+  float x[8];
+  raw.get(x);
   bool bad = false;
   float amax = 0.0f;
 #pragma unroll
@@ -129,10 +131,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 //    multiples of 2^-12 is therefore the half itself or on the quotient's side of it, and the second rounding,
 //    to integers, is that of the quotient.
 // Borders, values that are not finite and scales below 2^-100, where products underflow and the quotient may
-// pass 7, make the warp divide; elsewhere the quotient is at most 7 (1 + 2^-8).  Dividing everywhere took 1.7
-// times as long (16,384 rows of 16 heads of 64).
+// pass 7, are left to divisions (*divide); elsewhere the quotient is at most 7 (1 + 2^-8).  Dividing everywhere
+// took 1.7 times as long (16,384 rows of 16 heads of 64).
 template <typename X>
-__device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits, bool* bad) {
+__device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits, bool* divide) {
   float x[8];
   raw.get(x);
   uint32_t am = raw.absmax();
@@ -140,14 +142,8 @@ __device__ __forceinline__ uint32_t quantize8(const X& raw, uint32_t* scale_bits
   am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
   const uint32_t q7 = __float_as_uint(__uint_as_float(am) * (1.0f / 7.0f));
   uint32_t sb = (q7 + 0x7fffu + ((q7 >> 16) & 1u)) >> 16;   // to the nearest bfloat16
-  *bad = false;
   const bool zero = am == 0;
-  if (__any_sync(0xffffffffu, am >= 0x7f800000u || (!X::kEightBits && (q7 & 0xffffu) - 0x7ffcu <= 8u) || (sb < (27u << 7) && !zero))) {
-    const uint2 r = quantize8_by_division(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]));
-    *scale_bits = r.y & 0xffffu;
-    *bad = r.y >> 31;
-    return r.x;
-  }
+  *divide = am >= 0x7f800000u || (!X::kEightBits && (q7 & 0xffffu) - 0x7ffcu <= 8u) || (sb < (27u << 7) && !zero);
   sb = zero ? 0x3f80u : sb;
   *scale_bits = sb;
   const float s = __uint_as_float(sb << 16), y = X::kEightBits ? rcp_approx(s) : __frcp_rn(s);
@@ -219,6 +215,29 @@ __device__ __forceinline__ BlockRows find_block_rows(const int32_t* cu, int B, i
   return sh;
 }
 
+// A run's rows once more by divisions (rare: out of the way of the loop's registers); x, codes and scale point
+// to the lane's share of the first step.  Returns whether it held a value that is not finite; whole warps call it.
+template <int DH, typename T>
+__device__ __noinline__ bool append_by_division(const T* x, int64_t ld_tok, uint32_t* codes, uint16_t* scale, int fit, bool is_v) {
+  const int lane = threadIdx.x & 31, oct = lane % kRowLanes<DH>, r = lane / kRowLanes<DH>;
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < kTaskRows<DH>; i += kStepRows<DH>) {
+    const bool there = i + r < fit;
+    typename Octet<T>::type v;
+    if (there) v.load(x + i * ld_tok);
+    else v.zero();
+    const uint2 q = quantize8_by_division(v);
+    const uint32_t w = is_v ? v_word<DH>(q.x, oct) : q.x;
+    bad |= q.y >> 31;
+    if (there) {
+      codes[i * (DH / 8)] = w;
+      if ((oct & 3) == 0) scale[i * (DH / kKv4Group)] = static_cast<uint16_t>(q.y);
+    }
+  }
+  return bad;
+}
+
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, bool counts) {
   grid_dep_trigger();
@@ -255,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, b
       uint32_t* codes = reinterpret_cast<uint32_t*>(t ? a.c.v_codes : a.c.k_codes) + (row0 + r) * (DH / 8) + (t ? v_word_at<DH>(oct) : k_word_at<DH>(oct));
       uint16_t* scale = (t ? a.c.v_scale : a.c.k_scale) + (row0 + r) * G + (oct >> 2);
       typename Octet<T>::type v[kSteps];
+      bool redo = false;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         if (kFull || k * kStepRows<DH> + r < fit) v[k].load(x + k * kStepRows<DH> * a.ld_tok);
@@ -263,15 +283,16 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_append_kernel(AppendArgs a, b
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         uint32_t sb;
-        bool nonfinite;
-        uint32_t w = quantize8(v[k], &sb, &nonfinite);
+        bool divide;
+        uint32_t w = quantize8(v[k], &sb, &divide);
         if (t) w = v_word<DH>(w, oct);
-        bad |= nonfinite;
+        redo |= divide;
         if (kFull || k * kStepRows<DH> + r < fit) {
           codes[k * kStepRows<DH> * (DH / 8)] = w;
           if ((oct & 3) == 0) scale[k * kStepRows<DH> * G] = static_cast<uint16_t>(sb);
         }
       }
+      if (__any_sync(0xffffffffu, redo)) bad |= append_by_division<DH>(x, a.ld_tok, codes, scale, fit, t);
     };
 #pragma unroll 1   // unrolled it is too large for the instruction cache
     for (int t = 0; t < 2; ++t) {
@@ -322,8 +343,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_token_kernel(AppendArgs a
     else x.zero();
     // per_row is a multiple of 8 lanes: a group's four lanes, and V's pairs of groups, have one tensor
     uint32_t sb;
-    bool bad;
-    const uint32_t w = quantize8(x, &sb, &bad), v = v_word<DH>(w, oct);
+    bool divide, bad = false;
+    uint32_t w = quantize8(x, &sb, &divide);
+    if (__any_sync(0xffffffffu, divide)) {
+      const uint2 q = quantize8_by_division(x);
+      w = q.x, sb = q.y & 0xffffu, bad = q.y >> 31;
+    }
+    const uint32_t v = v_word<DH>(w, oct);
     if (ok) {
       if (bad) report(a.status, SPATTEN_E_NONFINITE);
       uint32_t* codes = reinterpret_cast<uint32_t*>(tensor ? a.c.v_codes : a.c.k_codes) + at * (DH / 8);
