@@ -1,7 +1,10 @@
 // spatten_kv4_attention: one query row per sequence over the 4-bit cache, grouped heads.
 //
-// A cluster of C CTAs owns one (sequence, key/value head); each CTA takes a run of its keys, each warp
-// tiles of TK keys, copied asynchronously into a ring of its own (no barriers in the loop).  The products
+// Up to a wave of CTAs, a cluster of C CTAs owns one (sequence, key/value head) and each CTA a run of its keys
+// (the cluster form); beyond it, all tiles of the call are dealt out evenly to two CTAs per SM, which leave
+// their parts and scores in the workspace for a second kernel that joins them (the split form: shape() has the
+// rule, both sides measured).  In both, each warp takes tiles of TK keys, copied asynchronously into a ring of
+// its own (no barriers in the loop).  The products
 // run on mma.sync m16n8k16 with the codes as the 16-row operand and up to 8 heads as the 8 columns:
 //   scores   S^T[16 keys][8 heads] = codes . q, one accumulator per group of 32 channels, which the
 //            group's scale then multiplies (so the codes enter exactly).  A nibble u = code + 8 in the
@@ -18,9 +21,12 @@
 // The tensor path is the register one since its operands are made in registers: a tcgen05 operand would
 // have to go through shared memory first, and the kernel is bound by memory and by the unpacking, not
 // by the products.
-// Scores stay in shared memory (in the workspace when they do not fit), so that the weights need only
-// one more exponential per score once the cluster has exchanged its maxima and sums.  Sums are float32
-// in a fixed order.
+// In the cluster form scores stay in shared memory (in the workspace when they do not fit), so that the
+// weights need only one more exponential per score once the cluster has exchanged its maxima and sums.  Sums
+// are float32 in a fixed order.
+// What bounds them: 16 x 1152 rows of 16 heads of 64, 11.3 us a call, the chain of one CTA (query, tiles, joining,
+// weights: 13,500 cycles); 32 x 16,384 rows of 8 heads of 128 with 4 queries each (478 MB), 140 us, unpacking codes
+// (the split kernel, 122 us: ALU pipe 58 %, 4.1 TB/s) and reading the scores back for the weights (22 us).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -918,7 +924,7 @@ constexpr size_t kSharedTwo = (113 - 16) * 1024, kSharedOne = (227 - 20) * 1024;
 
 // One launch of clusters: enough CTAs to fill the SMs, none with less than a tile per warp, and scores that let two
 // CTAs share an SM where more CTAs achieve that.  What takes more than one wave of them, or has scores that fit no
-// SM, is split instead (32 x 16384 rows, 8 heads of 128 with 4 queries each: <T_SPLIT> against 174 us; batches of
+// SM, is split instead (32 x 16384 rows, 8 heads of 128 with 4 queries each: 140 against 174 us; batches of
 // more than 1024 sequences, through which every CTA would have to look, are not).
 Shape shape(const spatten_kv4_attn_args& a) {
   Shape s{};

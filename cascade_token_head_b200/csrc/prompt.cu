@@ -33,7 +33,8 @@ int32_t validate(const spatten_prompt_args& a) {
   return SPATTEN_OK;
 }
 
-// Tensor cores wherever they can run, down to single rows.
+// Tensor cores wherever they can run, down to single rows (float32: 16 prompts of 512, 16 heads of 64, 168 against
+// 570 us; 77 to 512 rows of 128 behind 1000 others, 145 against 603).
 bool use_tc(const spatten_prompt_args& a) { return a.kernel != SPATTEN_ATTN_CUDA_CORE && prompt_tc_supported(a); }
 
 size_t layout(const spatten_prompt_args& a, void* ws, size_t ws_bytes, PromptProblem* p) {

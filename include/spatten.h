@@ -376,12 +376,16 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  *  - weight rows j >= weight_cap are not written and reported (SPATTEN_E_INDEX).
  *  - o overlaps none of the inputs.
  *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
- *  strides; workspace of spatten_prompt_workspace_size() bytes (0 without weight), which holds only this call's
+ *  strides; workspace of spatten_prompt_workspace_size() bytes (0 for bfloat16 without weight; float32
+ *  operands are laid out there as bfloat16 terms, 6 bytes an element), which holds only this call's
  *  intermediates: calls that overlap on the GPU need one each.
+ *  Kernels: AUTO takes the tensor cores, for float32 as sums of three bfloat16 terms an operand, whose
+ *  products keep 24 bits; CUDA_CORE multiplies and adds in float32; TENSOR_CORE by name is for bfloat16
+ *  (SPATTEN_E_UNSUPPORTED otherwise).
  * ============================================================================================= */
 typedef struct spatten_prompt_args {
   int32_t B, H, H_kv, d_h;
-  int32_t total_q, total_kv;  /* rows of the packed blocks; 0 rows are allowed                 */
+  int32_t total_q, total_kv;  /* rows of the packed blocks; 0 rows (and then no address) will do */
   const int32_t* cu_q;        /* device [B+1]: first query row of each sequence, then the end  */
   const int32_t* cu_kv;       /* device [B+1] for the key rows, or NULL: the same as cu_q      */
   int32_t dtype;              /* q, k, v and o: SPATTEN_F32 or SPATTEN_BF16                     */
