@@ -122,6 +122,18 @@ __device__ __forceinline__ void report(int32_t* st, int32_t code) {
   if (st) atomicCAS(st, 0, code);
 }
 
+// 32 bytes to a 16-byte aligned address, in one piece where it is a multiple of 32 (whole sectors)
+__device__ __forceinline__ void store32(void* p, const uint32_t* x) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                 "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 __device__ __forceinline__ float ld_as_float(const float* p) { return *p; }
 __device__ __forceinline__ float ld_as_float(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 

@@ -400,12 +400,15 @@ struct ReadArgs {
 // Stores the eight codes of a word times a scale (bfloat16 bits).
 __device__ __forceinline__ void store_values(float* p, uint32_t w, uint32_t sb) {
   const float s = bf16_bits_to_float(sb);
-  float x[8];
+  uint32_t x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)   // 2^23 + u, less 2^23 + 8
-    x[i] = s * (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f);
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  for (int i = 0; i < 8; i += 2) {   // 2^23 + u, less 2^23 + 8
+    const float2 u = make_float2(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u), __uint_as_float(((w >> (4 * i + 4)) & 15u) | 0x4b000000u));
+    const float2 v = __fmul2_rn(__fadd2_rn(u, make_float2(-8388616.0f, -8388616.0f)), make_float2(s, s));
+    x[i] = __float_as_uint(v.x), x[i + 1] = __float_as_uint(v.y);
+  }
+  // whole sectors where the address allows it (18 x 330 rows of 12 heads of 128, 73 MB: 14.9 us, halves 21.4)
+  store32(p, x);
 }
 // In bfloat16 the code is exact and the product is rounded once, as the float32 product would be.
 __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint32_t sb) {

@@ -764,3 +764,21 @@ print("same bits")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, PYTHONPATH=root), capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and "same bits" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift,wide", [(0, 4), (4, 0), (4, 4)])
+def test_float32_rows_at_16_byte_addresses(cuda, d, shift, wide):
+    """float32 rows whose addresses are multiples of 16 bytes, not of 32: append and read give the exact rows."""
+    S, H, n = lib(), 3, 50
+    ld = H * d + wide
+    x = torch.randn((n * ld + shift,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(d + wide))
+    rows = x[shift:].view(n, ld)
+    c, ln, status = Cache(S, 2, H, d, 40, seed=d), i32([0, 3]), i32([0])
+    S.kv4_append(c.c, rows, rows, ld, n, ln, ln, ln.clone(), ln.clone(), cu=i32([0, 21, 50]), dev_status=status)
+    out = torch.full((n * ld + shift,), 7.0, device="cuda")
+    got = out[shift:].view(n, ld)
+    S.kv4_read(c.c, i32([0, 21, 50]), n, got, None, ld, row0=i32([0, 3]), dev_status=status)
+    code, s = R.quantize4(rows[:, :H * d].unflatten(1, (H, d)).cpu().numpy())
+    np.testing.assert_array_equal(host(got)[:, :H * d].reshape(n, H, d), code.astype(np.float64) * np.repeat(s, 32, axis=-1).astype(np.float64))
+    assert (host(got)[:, H * d:] == 7).all() and (host(out)[:shift] == 7).all() and int(status.item()) == 0
