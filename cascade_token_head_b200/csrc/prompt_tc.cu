@@ -580,9 +580,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       if constexpr (PL == 3) {
         if (r < my_rows)
 #pragma unroll
-          for (int j = 0; j < DH; j += 4)
-            dst[j / 4] = make_uint4(__float_as_uint(acc[j] * inv), __float_as_uint(acc[j + 1] * inv), __float_as_uint(acc[j + 2] * inv),
-                                    __float_as_uint(acc[j + 3] * inv));
+          for (int j = 0; j < DH; j += 8) {
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(acc[j + i] * inv);
+            store32(dst + j / 4, u);
+          }
       } else {
 #pragma unroll 1
         for (int ch = 0; ch < kOCols / 32; ++ch) {
@@ -596,9 +599,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           }
           if (r < my_rows) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[ch * 4 + q] = make_uint4(pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv), pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                           pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv), pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+            for (int q = 0; q < 2; ++q) {
+              uint32_t u[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
+              store32(dst + ch * 4 + 2 * q, u);
+            }
           }
         }
       }

@@ -782,3 +782,10 @@ def test_float32_rows_at_16_byte_addresses(cuda, d, shift, wide):
     code, s = R.quantize4(rows[:, :H * d].unflatten(1, (H, d)).cpu().numpy())
     np.testing.assert_array_equal(host(got)[:, :H * d].reshape(n, H, d), code.astype(np.float64) * np.repeat(s, 32, axis=-1).astype(np.float64))
     assert (host(got)[:, H * d:] == 7).all() and (host(out)[:shift] == 7).all() and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64), (F32, 128)])
+def test_prompt_rows_at_16_byte_addresses(cuda, dtype, d):
+    """Rows whose addresses are multiples of 16 bytes, not of 32."""
+    Prompt(lib(), dtype, d, 3, 3, [60, 150], [60, 190], seed=18, front=1, back=2,
+           wide=8 if dtype == BF else 4).run().check(UBF if dtype == BF else 0.0)
