@@ -789,3 +789,30 @@ def test_prompt_rows_at_16_byte_addresses(cuda, dtype, d):
     """Rows whose addresses are multiples of 16 bytes, not of 32."""
     Prompt(lib(), dtype, d, 3, 3, [60, 150], [60, 190], seed=18, front=1, back=2,
            wide=8 if dtype == BF else 4).run().check(UBF if dtype == BF else 0.0)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,top", [(25, 200), (50, 1100)])
+def test_evict_many_heads(cuda, in_place, B, top):
+    """More (sequence, head) pairs than two CTAs an SM hold."""
+    S, H, d, keep, recent = lib(), 12, 64, 60, 9
+    r = np.random.default_rng(B)
+    n = r.integers(0, top, B)
+    n[:3] = 0, keep, top
+    cap = top + 1
+    c = Cache(S, B, H, d, cap, seed=B)
+    c.t["weight"].copy_(torch.round(c.t["weight"] * 8) / 8)      # ties
+    before = c.host()
+    dst = c if in_place else Cache(S, B, H, d, keep, seed=1)
+    ln, status = i32(n.tolist()), i32([0])
+    out = ln if in_place else torch.zeros_like(ln)
+    nb = S.kv4_evict_workspace_size(c.c, cap, keep)
+    S.kv4_evict(c.c, dst.c, ln, out, i32(n.tolist()), cap, keep, recent, ws(nb), nb, dev_status=status)
+    torch.cuda.synchronize()
+    got = dst.host()
+    for b in range(B):
+        for h in range(0, H, 5):
+            src = R.evict_sources(before["weight"][b, h], before["pos"][b, h], int(n[b]), int(n[b]), keep, recent)
+            for key in got:
+                np.testing.assert_array_equal(got[key][b, h, :len(src)], before[key][b, h, src], err_msg=f"{key} {b} {h}")
+    assert out.tolist() == np.minimum(n, keep).tolist() and int(status.item()) == 0
