@@ -816,3 +816,28 @@ def test_evict_many_heads(cuda, in_place, B, top):
             for key in got:
                 np.testing.assert_array_equal(got[key][b, h, :len(src)], before[key][b, h, src], err_msg=f"{key} {b} {h}")
     assert out.tolist() == np.minimum(n, keep).tolist() and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_prompt_nonfinite_sequences_next_to_finite_ones(cuda, dtype, d, kernel):
+    """Every second of 36 sequences holds NaN and infinities; the others' outputs and weights are theirs alone."""
+    S, B = lib(), 36
+    r = np.random.default_rng(d)
+    lens, old = r.integers(1, 140, B), r.integers(0, 90, B)
+    p = Prompt(S, dtype, d, 2, 1, lens.tolist(), (lens + old).tolist(), seed=19, kernel=kernel)
+    for b in range(1, B, 2):
+        p.qb[p.cu_q[b]:p.cu_q[b + 1]] = float("inf")
+        p.kb[p.cu_kv[b]:p.cu_kv[b + 1]] = float("nan")
+        p.vb[p.cu_kv[b]:p.cu_kv[b + 1]] = float("-inf")
+    p.run()
+    q, k, v = host(p.q), host(p.k), host(p.v)
+    for b in range(0, B, 2):
+        rows, keys = slice(p.cu_q[b], p.cu_q[b + 1]), slice(p.cu_kv[b], p.cu_kv[b + 1])
+        n_q, n = p.cu_q[b + 1] - p.cu_q[b], p.cu_kv[b + 1] - p.cu_kv[b]
+        ref, w = R.prompt_attention(q[rows], k[keys], v[keys], [0, n_q], [0, n], p.n_w)
+        spread, _ = R.prompt_attention(q[rows], k[keys], np.abs(v[keys]), [0, n_q], [0, n], p.n_w)
+        e = score_step(q[rows], k[keys], n)
+        check_out(host(p.o)[rows], ref, spread, e, dtype, UBF if dtype == BF and kernel == 0 else 0.0, f"sequence {b}")
+        check_weight(host(p.w)[b], host(p.w0)[b], w[0], e, f"sequence {b}")
+    assert int(p.status.item()) == 0
