@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         mbar_arrive(&bars.v_fix);
       }
     }
-    if (aborted && lane == 0 && Tmax > 0) {   // the copies in flight land before shared memory is given up
+    if (lane == 0 && Tmax > 0) {   // copies in flight land before shared memory is given up, whoever gave up waiting
       drain_wait(&bars.q_full, 0);
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.kv_full[x % NST], (x / NST) & 1);
     }
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
       ++issued;
     }
     __syncwarp();
-    if (aborted && lane == 0) {
+    if (lane == 0 && NT > 0) {   // as in the output kernel
       drain_wait(&bars.k_full, 0);
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.q_full[x % NST], (x / NST) & 1);
     }
