@@ -40,7 +40,8 @@ bool use_tc(const spatten_prompt_args& a) { return a.kernel != SPATTEN_ATTN_CUDA
 size_t layout(const spatten_prompt_args& a, void* ws, size_t ws_bytes, PromptProblem* p) {
   const bool tc = use_tc(a);
   const bool split = tc && a.dtype == SPATTEN_F32 && a.total_q > 0;
-  if (!a.weight && !split) return 0;
+  const int splits = tc && a.total_q > 0 ? prompt_tc_splits(a) : 1;
+  if (!a.weight && !split && splits == 1) return 0;
   WsCursor c(ws, ws_bytes);
   uint16_t* planes[3] = {};
   if (split)
@@ -50,8 +51,12 @@ size_t layout(const spatten_prompt_args& a, void* ws, size_t ws_bytes, PromptPro
   float* offset = a.weight && tc ? c.take<float>(rows) : nullptr;
   float2* stats = a.weight && !tc ? c.take<float2>(rows) : nullptr;
   float* part = a.weight && a.H > a.H_kv ? c.take<float>(static_cast<size_t>(a.H) * a.total_kv) : nullptr;
+  const size_t parts = splits > 1 ? static_cast<size_t>(splits) * a.H * a.total_q : 0;
+  float2* split_ml = parts ? c.take<float2>(parts) : nullptr;
+  float* split_o = parts ? c.take<float>(parts * a.d_h) : nullptr;
   if (p) {
     for (int t = 0; t < 3; ++t) p->planes[t] = planes[t];
+    p->splits = splits, p->split_ml = split_ml, p->split_o = split_o;
     p->offset = offset, p->stats = stats, p->part = part;
   }
   return align_up(c.used, 256);
@@ -101,6 +106,7 @@ extern "C" int32_t spatten_prompt_attention(const spatten_prompt_args* a, void* 
   PromptProblem p{};
   p.a = *a;
   p.wait_limit = std::min(wait_limit_setting(), kPromptWaitLimit);
+  p.splits = 1;
   const size_t need = layout(*a, ws, ws_bytes, &p);
   if (need && (!ws || ws_bytes < need)) return SPATTEN_E_WORKSPACE;
   if (need && !aligned16(ws)) return SPATTEN_E_ALIGN;

@@ -15,6 +15,10 @@ struct PromptProblem {
   float* offset;
   uint16_t* planes[3];     // float32 on tensor cores: q, k, v as [3][rows][heads][d_h] bfloat16 terms
   float* part;             // [H][total_kv] the heads' column sums (grouped heads)
+  // few rows against long sequences: the key tiles of a row tile are dealt to `splits` CTAs (else 1), which leave
+  int32_t splits;
+  float2* split_ml;        // [splits][H][total_q] maximum (log2 units) and sum of each row
+  float* split_o;          // [splits][H][total_q][d_h] and its output, relative to that maximum
   uint32_t wait_limit;     // polls of one pipeline wait (tensor-core kernels)
 };
 
@@ -91,5 +95,6 @@ int32_t prompt_simt_launch(const PromptProblem& p, cudaStream_t st);
 int32_t prompt_reduce_launch(const PromptProblem& p, cudaStream_t st);   // weight += the heads' column sums
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st);
 bool prompt_tc_supported(const spatten_prompt_args& a);
+int prompt_tc_splits(const spatten_prompt_args& a);
 
 }  // namespace spt

@@ -15,6 +15,8 @@
 //          scores, transposed: S^T = K Q^T puts one key on each TMEM lane, so the sum over the rows stays
 //          inside a thread (no exchange between lanes) and runs in a fixed order.
 //  The heads of a group add up in a third, small one.
+//  Where a call has too few row tiles to fill the GPU and long sequences, each tile's keys are split over several
+//  CTAs of OUTPUT, whose parts a JOIN kernel adds up with the weights exp(m_part - m).
 // What bounds them: exponentials (16 per clock and SM; for the weights a quarter of them goes to the FMA
 // pipe, exp2_poly.cuh) next to the tensor cores.  8192 tokens, 32 heads of 128 over 8 (550 GFLOP): output
 // 487 us in a row of calls, 1127 TFLOP/s, where the power limit holds the clock down (440 us by itself, tensor pipe
@@ -198,12 +200,15 @@ struct OutBars {
   uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[NQ], p_ready[NQ], o_full[NQ], v_fix, drain;
 };
 
+constexpr int kSplitTiles = 4, kMaxSplits = 16;   // key tiles that a split has at least, splits at most
+
 // What a CTA does with its tile.
 template <class C>
 struct OutWork {
   int head[C::NQ], row0[C::NQ], rows[C::NQ], T[C::NQ];   // of each query tile: head, rows of the sequence, key tiles seen
   int Tmax, partial;                                     // the most key tiles; the one that ends past the keys, or -1
-  __device__ __forceinline__ OutWork(const PromptTile& pt, int slot, bool pair_heads, int tile_rows) {
+  int key0;                                              // the first key: of all those tiles, or of split `part` of `parts`
+  __device__ __forceinline__ OutWork(const PromptTile& pt, int slot, bool pair_heads, int tile_rows, int part, int parts) {
     Tmax = 0;
 #pragma unroll
     for (int g = 0; g < C::NQ; ++g) {
@@ -215,10 +220,20 @@ struct OutWork {
       Tmax = max(Tmax, T[g]);
     }
     partial = pt.k.n < Tmax * C::KT ? Tmax - 1 : -1;
+    key0 = 0;
+    if (parts > 1) {
+      const int per = max(kSplitTiles, (Tmax + parts - 1) / parts), lo = part * per;
+      key0 = lo * C::KT;
+      Tmax = max(0, min(Tmax - lo, per));
+#pragma unroll
+      for (int g = 0; g < C::NQ; ++g) T[g] = max(0, min(T[g] - lo, per));
+      partial = partial >= lo && partial - lo < Tmax ? partial - lo : -1;
+    }
   }
 };
 
-template <class C>
+// SPLIT: the CTA has a part of its row tile's keys (a kernel of its own: it costs registers, 2 % of unsplit calls)
+template <class C, bool SPLIT>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(PromptProblem p, const __grid_constant__ Maps maps) {
   constexpr int DH = C::DH, NQ = C::NQ, KT = C::KT, PL = C::PL, NST = C::kStages, kHalves = C::kHalves;
   extern __shared__ uint8_t smem_raw[];
@@ -263,6 +278,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   grid_dep_wait();
   if (blockIdx.x == 0) report_bad_offsets(a);
   // one warp looks the tile up and starts the loads that wait for nothing, before the CTA meets
+  const int parts = SPLIT ? p.splits : 1, part = SPLIT ? static_cast<int>(blockIdx.x / slots) % parts : 0;
   const int slot = blockIdx.x % slots, hk = (pair_heads ? 2 * slot : slot) / G;
   auto load_kv = [&](int x, int first) {   // the ring's x-th tile: K0 V0 K1 V1 ..
     mbar_arrive_expect_tx(&bars.kv_full[x % NST], C::kTile);
@@ -270,18 +286,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
                           &bars.kv_full[x % NST]);
   };
   if (warp == kProducer) {
-    const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots);
+    const PromptTile pt = find_prompt_tile<false>(a, tile_rows, blockIdx.x / slots / parts);
     if (lane == 0) {
       item = pt;
       if (pt.b >= 0) {
-        const OutWork<C> w(pt, slot, pair_heads, tile_rows);
+        const OutWork<C> w(pt, slot, pair_heads, tile_rows, part, parts);
         if (w.Tmax > 0) {
           mbar_arrive_expect_tx(&bars.q_full, NQ * C::kQTile);
 #pragma unroll
           for (int g = 0; g < NQ; ++g)   // a tile without rows is loaded from the first one's rows and not used
             load_tile<DH, kRows, PL>(smem + g * C::kQTile, &maps.q, w.head[g], pt.q.first + (w.rows[g] ? w.row0[g] : w.row0[0]), a.total_q,
                                      &bars.q_full);
-          for (int x = 0; x < min(NST, 2 * w.Tmax); ++x) load_kv(x, pt.k.first);
+          for (int x = 0; x < min(NST, 2 * w.Tmax); ++x) load_kv(x, pt.k.first + w.key0);
         }
       }
     }
@@ -298,7 +314,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
   }
   const PackedRows qr = pt.q, kr = pt.k;
   const int shift = kr.n - qr.n;
-  const OutWork<C> work(pt, slot, pair_heads, tile_rows);
+  const OutWork<C> work(pt, slot, pair_heads, tile_rows, part, parts);
   const auto &head = work.head, &row0 = work.row0, &rows = work.rows, &T = work.T;
   const int Tmax = work.Tmax, partial = work.partial, early = min(NST, 2 * Tmax);
   bool aborted = false;
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           aborted = true;
           break;
         }
-        if (lane == 0) load_kv(x, kr.first);
+        if (lane == 0) load_kv(x, kr.first + work.key0);
         ++issued;
       }
       if ((x & 1) && t == partial) {
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
           aborted = true;
           break;
         }
-        const int first = kr.n - t * KT;
+        const int first = kr.n - work.key0 - t * KT;
         for (int e = first * 8 + lane; e < KT * 8; e += 32)
 #pragma unroll
           for (int c = 0; c < PL * DH / 64; ++c)
@@ -421,7 +437,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       const bool ok = warp_wait(&bars.s_full[g], t & 1, abort_flag, wlim);
       tc_after_sync();
       if (PL == 3 && ok && t > 0) add_tile();   // the score MMA was issued behind the previous P V
-      const int j0 = t * KT + half * 64, lim = last - j0;   // columns 0 .. lim are seen
+      const int j0 = work.key0 + t * KT + half * 64, lim = last - j0;   // columns 0 .. lim are seen
       const bool full = last_first - j0 >= 63;              // by every row of the warp
       float mx = -INFINITY;
       if (ok) {   // the scores are read twice: there are not registers enough to keep them over the vote
@@ -576,40 +592,67 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
       const int64_t row = static_cast<int64_t>(qr.first) + my_row0 + r;
       using T = std::conditional_t<PL == 1, __nv_bfloat16, float>;
       if (PL == 3 && my_T > 0) add_tile();
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
-      if constexpr (PL == 3) {
-        if (r < my_rows)
+      if constexpr (SPLIT) {   // as it is: prompt_join_kernel does the rest
+        const int64_t at = (static_cast<int64_t>(part) * a.H + my_head) * a.total_q + row;
+        if (r < my_rows && half == 0) p.split_ml[at] = make_float2(m, l);
+        if (my_T > 0) {
+          float* part_o = p.split_o + at * DH + half * kOCols;
 #pragma unroll
-          for (int j = 0; j < DH; j += 8) {
-            uint32_t u[8];
+          for (int ch = 0; ch < kOCols; ch += 32) {
+            float o[32];
+            if constexpr (PL == 3) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(acc[j + i] * inv);
-            store32(dst + j / 4, u);
+              for (int j = 0; j < 32; ++j) o[j] = acc[ch + j];
+            } else {
+              tmem_ld32(tO + ch, o);
+              tmem_ld_wait();
+            }
+            if (r < my_rows)
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(o[j + i]);
+                store32(part_o + ch + j, u);
+              }
           }
+        }
       } else {
-#pragma unroll 1
-        for (int ch = 0; ch < kOCols / 32; ++ch) {
-          float o[32];
-          if (my_T > 0) {
-            tmem_ld32(tO + ch * 32, o);
-            tmem_ld_wait();
-          } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(my_head) * DH + half * kOCols);
+        if constexpr (PL == 3) {
+          if (r < my_rows)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-          }
-          if (r < my_rows) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int j = 0; j < DH; j += 8) {
               uint32_t u[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
-              store32(dst + ch * 4 + 2 * q, u);
+              for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(acc[j + i] * inv);
+              store32(dst + j / 4, u);
+            }
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < kOCols / 32; ++ch) {
+            float o[32];
+            if (my_T > 0) {
+              tmem_ld32(tO + ch * 32, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+            }
+            if (r < my_rows) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
+                store32(dst + ch * 4 + 2 * q, u);
+              }
             }
           }
         }
+        if (p.offset && half == 0 && r < my_rows)   // exp2(c (S + offset)) = P
+          p.offset[static_cast<int64_t>(my_head) * a.total_q + row] = l > 0.0f ? -(m + log2f(l)) / c : (l == 0.0f ? 0.0f : l);
       }
-      if (p.offset && half == 0 && r < my_rows)   // exp2(c (S + offset)) = P
-        p.offset[static_cast<int64_t>(my_head) * a.total_q + row] = l > 0.0f ? -(m + log2f(l)) / c : (l == 0.0f ? 0.0f : l);
     }
   }
   tc_before_sync();
@@ -619,6 +662,43 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
     tc_after_sync();
     tmem_dealloc(tmem, C::kTmem);
   }
+}
+
+// The splits of a row joined: a warp per row and head, DH / 32 channels a lane.
+template <int DH, typename T>
+__global__ void __launch_bounds__(256) prompt_join_kernel(PromptProblem p) {
+  grid_dep_trigger();
+  grid_dep_wait();
+  const spatten_prompt_args& a = p.a;
+  constexpr int N = DH / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int row = static_cast<int>(x / a.H), h = static_cast<int>(x % a.H);
+  if (row >= a.total_q) return;
+  const int b = owner_of_row(a.cu_q, a.B, row);
+  if (b < 0) return;
+  const PackedRows qr = packed_rows(a.cu_q, b, a.total_q);
+  if (qr.bad || row < qr.first || row - qr.first >= qr.n) return;   // rows of no sequence stay as they are
+  const int64_t at = static_cast<int64_t>(h) * a.total_q + row, step = static_cast<int64_t>(a.H) * a.total_q;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.split_ml[s * step + at].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f, o[N] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.split_ml[s * step + at];
+    if (ml.y == 0.0f) continue;   // no key (and no output written); a NaN goes on
+    const float f = ex2(ml.x - base);
+    l = fmaf(ml.y, f, l);
+    const float* part = p.split_o + (s * step + at) * DH + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(part[i], f, o[i]);
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  T* dst = static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(h) * DH + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) st_from_float(dst + i, o[i] * inv);
+  if (p.offset && lane == 0)   // as in the output kernel
+    p.offset[at] = l > 0.0f ? -(m + log2f(l)) / (a.sm_scale * kLog2e) : (l == 0.0f ? 0.0f : l);
 }
 
 // =================================================================================================
@@ -934,12 +1014,30 @@ int32_t make_map(CUtensorMap* m, const void* base, int dh, int heads, int rows, 
   return r == CUDA_SUCCESS ? SPATTEN_OK : SPATTEN_E_UNSUPPORTED;
 }
 
+// CTAs of the output kernel that cover any offsets: a sequence's rows end in at most one partial tile.
+template <class O>
+int64_t out_blocks(const spatten_prompt_args& a) {
+  const bool pair_heads = O::NQ == 2 && (a.H / a.H_kv) % 2 == 0;
+  const int tile_rows = O::NQ == 2 && !pair_heads ? 256 : 128;
+  return (static_cast<int64_t>(a.total_q) / tile_rows + a.B) * (pair_heads ? a.H / 2 : a.H);
+}
+
+// Splits of the key tiles: as many as leave all CTAs resident at once and each kSplitTiles tiles of a sequence of
+// average length (16 rows of 16 heads of 64 behind 8000 others: 23 against 111 us; 500 of 8 heads behind 1500: 23
+// against 32).
+template <class O>
+int out_splits(const spatten_prompt_args& a) {
+  const int64_t most = std::min<int64_t>(O::kCtas * sm_count() / std::max<int64_t>(1, out_blocks<O>(a)), a.total_kv / std::max(1, a.B) / (kSplitTiles * O::KT));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, most)));
+}
+
 template <class O, class W>
 int32_t launch(const PromptProblem& p, cudaStream_t st) {
   static DeviceOnce once;
   int dev;
   SPT_TRY(once_per_device(once, &dev, [](int) -> int32_t {
-    SPT_CUDA(cudaFuncSetAttribute(prompt_out_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, O::kSmem));
+    SPT_CUDA(cudaFuncSetAttribute(prompt_out_kernel<O, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, O::kSmem));
+    SPT_CUDA(cudaFuncSetAttribute(prompt_out_kernel<O, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, O::kSmem));
     SPT_CUDA(cudaFuncSetAttribute(prompt_weight_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem));
     return SPATTEN_OK;
   }));
@@ -958,13 +1056,15 @@ int32_t launch(const PromptProblem& p, cudaStream_t st) {
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_div(octets, 256), 16 * sm_count()));
     SPT_TRY(launch_chained(prompt_split_kernel, dim3(blocks, 3), dim3(256), 0, st, 1, p));
   }
-  const bool pair_heads = O::NQ == 2 && (a.H / a.H_kv) % 2 == 0;
-  const int tile_rows = O::NQ == 2 && !pair_heads ? 256 : 128;
-  // a sequence's rows end in at most one partial tile, so this many tiles cover any offsets
-  const int64_t q_blocks = (static_cast<int64_t>(a.total_q) / tile_rows + a.B) * (pair_heads ? a.H / 2 : a.H);
+  const int64_t q_blocks = out_blocks<O>(a) * p.splits;
   const int64_t k_blocks = (static_cast<int64_t>(a.total_kv) / kRows + a.B) * a.H;
   if (q_blocks > INT32_MAX || k_blocks > INT32_MAX) return SPATTEN_E_UNSUPPORTED;
-  SPT_TRY(launch_chained(prompt_out_kernel<O>, dim3(static_cast<unsigned>(q_blocks)), dim3(O::kThreads), O::kSmem, st, 1, p, maps));
+  const auto out = p.splits > 1 ? prompt_out_kernel<O, true> : prompt_out_kernel<O, false>;
+  SPT_TRY(launch_chained(out, dim3(static_cast<unsigned>(q_blocks)), dim3(O::kThreads), O::kSmem, st, 1, p, maps));
+  if (p.splits > 1) {
+    const auto join = prompt_join_kernel<O::DH, std::conditional_t<O::PL == 1, __nv_bfloat16, float>>;
+    SPT_TRY(launch_chained(join, dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.total_q) * a.H, 8))), dim3(256), 0, st, 1, p));
+  }
   if (!a.weight) return SPATTEN_OK;
   SPT_TRY(launch_chained(prompt_weight_kernel<W>, dim3(static_cast<unsigned>(k_blocks)), dim3(W::kThreads), W::kSmem, st, 1, p, maps));
   if (a.H == a.H_kv) return SPATTEN_OK;
@@ -980,11 +1080,24 @@ bool prompt_tc_supported(const spatten_prompt_args& a) {
                                  : a.total_q <= INT32_MAX / 4 && a.total_kv <= INT32_MAX / 4;
 }
 
+namespace {
+
+// The tiles of a type and head size: call(output tiles, weight tiles).
+template <typename F>
+auto with_tiles(const spatten_prompt_args& a, F&& call) {
+  if (a.dtype == SPATTEN_BF16)
+    return a.d_h == 64 ? call(OutCfg<64, 1, 64, 4>{}, WeightCfg<64, 2, 1, 3>{}) : call(OutCfg<128, 2, 128, 4>{}, WeightCfg<128, 1, 1, 3>{});
+  return a.d_h == 64 ? call(OutCfg<64, 1, 64, 2, 3>{}, WeightCfg<64, 1, 2, 2, 3>{}) : call(OutCfg<128, 1, 64, 2, 3>{}, WeightCfg<128, 1, 2, 1, 3>{});
+}
+
+}  // namespace
+
+int prompt_tc_splits(const spatten_prompt_args& a) {
+  return with_tiles(a, [&](auto o, auto) { return out_splits<decltype(o)>(a); });
+}
+
 int32_t prompt_tc_launch(const PromptProblem& p, cudaStream_t st) {
-  if (p.a.dtype == SPATTEN_BF16)
-    return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 4>, WeightCfg<64, 2, 1, 3>>(p, st) : launch<OutCfg<128, 2, 128, 4>, WeightCfg<128, 1, 1, 3>>(p, st);
-  return p.a.d_h == 64 ? launch<OutCfg<64, 1, 64, 2, 3>, WeightCfg<64, 1, 2, 2, 3>>(p, st)
-                       : launch<OutCfg<128, 1, 64, 2, 3>, WeightCfg<128, 1, 2, 1, 3>>(p, st);
+  return with_tiles(p.a, [&](auto o, auto w) { return launch<decltype(o), decltype(w)>(p, st); });
 }
 
 }  // namespace spt

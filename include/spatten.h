@@ -376,9 +376,10 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  *  - weight rows j >= weight_cap are not written and reported (SPATTEN_E_INDEX).
  *  - o overlaps none of the inputs.
  *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
- *  strides; workspace of spatten_prompt_workspace_size() bytes (0 for bfloat16 without weight; float32
- *  operands are laid out there as bfloat16 terms, 6 bytes an element), which holds only this call's
- *  intermediates: calls that overlap on the GPU need one each.
+ *  strides; workspace of spatten_prompt_workspace_size() bytes (it may be 0), which holds only this call's
+ *  intermediates -- the rows' statistics for the weights, float32 operands as bfloat16 terms (6 bytes an
+ *  element), the parts of few rows whose long key sequences are split over CTAs: calls that overlap on the
+ *  GPU need one each.
  *  Kernels: AUTO takes the tensor cores, for float32 as sums of three bfloat16 terms an operand, whose
  *  products keep 24 bits; CUDA_CORE multiplies and adds in float32; TENSOR_CORE by name is for bfloat16
  *  (SPATTEN_E_UNSUPPORTED otherwise).

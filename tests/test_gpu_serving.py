@@ -841,3 +841,32 @@ def test_prompt_nonfinite_sequences_next_to_finite_ones(cuda, dtype, d, kernel):
         check_out(host(p.o)[rows], ref, spread, e, dtype, UBF if dtype == BF and kernel == 0 else 0.0, f"sequence {b}")
         check_weight(host(p.w)[b], host(p.w0)[b], w[0], e, f"sequence {b}")
     assert int(p.status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("H,Hk,lens,kv", [
+    (2, 2, [5], [2500]), (6, 2, [1], [1025]), (3, 1, [300], [5000]), (4, 2, [40, 1, 0, 130], [900, 2900, 2000, 131]),
+    (2, 1, [2, 20, 9], [6000, 10, 0])])
+def test_prompt_few_rows_over_long_histories(cuda, dtype, d, H, Hk, lens, kv):
+    """The keys of a row tile may be split over CTAs: ends inside a tile, splits without keys, sequences without any."""
+    Prompt(lib(), dtype, d, H, Hk, lens, kv, seed=20, front=2, back=3).run().check(UBF if dtype == BF else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prompt_split_without_weights_repeats_its_bits(cuda, dtype):
+    S = lib()
+    p = Prompt(S, dtype, 64, 4, 4, [7, 30], [4000, 3000], seed=21)
+    a = S.make_prompt_args(p.q, p.k, p.v, p.o, i32(p.cu_q), i32(p.cu_kv), dev_status=p.status)
+    nb = S.prompt_workspace_size(a)
+    first = None
+    for fill in (0, 255, 127):      # whatever the workspace held
+        p.o.fill_(7)
+        w = torch.full((nb + 256,), fill, dtype=torch.uint8, device="cuda")
+        S.prompt_attention(a, w, nb)
+        torch.cuda.synchronize()
+        assert (w[nb:] == fill).all()
+        first = p.o.clone() if first is None else first
+        assert torch.equal(first, p.o)
+    ref, _ = R.prompt_attention(host(p.q), host(p.k), host(p.v), p.cu_q, p.cu_kv, 1)
+    spread, _ = R.prompt_attention(host(p.q), host(p.k), np.abs(host(p.v)), p.cu_q, p.cu_kv, 1)
+    check_out(host(p.o), ref, spread, score_step(host(p.q), host(p.k), 4000), dtype, UBF if dtype == BF else 0.0)
