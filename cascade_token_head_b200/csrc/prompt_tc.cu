@@ -200,7 +200,7 @@ struct OutBars {
   uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[NQ], p_ready[NQ], o_full[NQ], v_fix, drain;
 };
 
-constexpr int kSplitTiles = 4, kMaxSplits = 16;   // key tiles that a split has at least, splits at most
+constexpr int kSplitTiles = 2, kMaxSplits = 16;   // key tiles that a split has at least, splits at most
 
 // What a CTA does with its tile.
 template <class C>
@@ -1023,8 +1023,8 @@ int64_t out_blocks(const spatten_prompt_args& a) {
 }
 
 // Splits of the key tiles: as many as leave all CTAs resident at once and each kSplitTiles tiles of a sequence of
-// average length (16 rows of 16 heads of 64 behind 8000 others: 23 against 111 us; 500 of 8 heads behind 1500: 23
-// against 32).
+// average length (16 rows of 16 heads of 64 behind 8000 others: 23 against 111 us; 500 of 8 heads behind 1500: 21
+// against 32; float32, 16 of 8 heads of 128 behind 1000: 25, with four tiles at least 34, unsplit 63).
 template <class O>
 int out_splits(const spatten_prompt_args& a) {
   const int64_t most = std::min<int64_t>(O::kCtas * sm_count() / std::max<int64_t>(1, out_blocks<O>(a)), a.total_kv / std::max(1, a.B) / (kSplitTiles * O::KT));
