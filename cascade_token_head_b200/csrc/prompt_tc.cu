@@ -200,7 +200,7 @@ struct OutBars {
   uint64_t q_full, kv_full[NST], kv_empty[NST], s_full[NQ], p_ready[NQ], o_full[NQ], v_fix, drain;
 };
 
-constexpr int kSplitTiles = 2, kMaxSplits = 16;   // key tiles that a split has at least, splits at most
+constexpr int kSplitTiles = 2, kMaxSplits = 32;   // key tiles that a split has at least, splits at most
 
 // What a CTA does with its tile.
 template <class C>
@@ -680,18 +680,24 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptProblem p) {
   const PackedRows qr = packed_rows(a.cu_q, b, a.total_q);
   if (qr.bad || row < qr.first || row - qr.first >= qr.n) return;   // rows of no sequence stay as they are
   const int64_t at = static_cast<int64_t>(h) * a.total_q + row, step = static_cast<int64_t>(a.H) * a.total_q;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.split_ml[s * step + at].x);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, o[N] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.split_ml[s * step + at];
-    if (ml.y == 0.0f) continue;   // no key (and no output written); a NaN goes on
-    const float f = ex2(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    const float* part = p.split_o + (s * step + at) * DH + lane * N;
+  static_assert(kMaxSplits <= 32, "a lane a split");
+  const float2 ml = lane < p.splits ? p.split_ml[lane * step + at] : make_float2(-INFINITY, 0.0f);
+  float m = ml.x;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(part[i], f, o[i]);
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  // a split without keys has l = 0 and left no output; a NaN goes on
+  const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - (m == -INFINITY ? 0.0f : m));
+  float l = 0.0f, o[N] = {};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float ls = __shfl_sync(0xffffffffu, ml.y, s), fs = __shfl_sync(0xffffffffu, f, s);
+    const float* part = p.split_o + (s * step + at) * DH + lane * N;
+    l = fmaf(ls, fs, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float v = ls == 0.0f ? 0.0f : part[i];
+      o[i] = fmaf(v, fs, o[i]);
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
   T* dst = static_cast<T*>(a.o) + row * a.o_ld_tok + static_cast<int64_t>(h) * DH + lane * N;
