@@ -1,7 +1,7 @@
 // The 4-bit cache's row layout and the bounds shared by its kernels (see spatten.h).
 #pragma once
 
-#include "common.cuh"
+#include "chained.cuh"
 
 namespace spt {
 

@@ -34,7 +34,7 @@
 #include "attention.cuh"
 #include "exp2_poly.cuh"
 #include "prompt.cuh"
-#include "tc_ptx.cuh"
+#include "tc_tma.cuh"
 
 namespace spt {
 namespace {

@@ -605,6 +605,8 @@ __device__ __forceinline__ int bin_of(float f, const BinMap& m) {
 // start).  grid_dep_wait() returns once the previous step's grid has completed and its writes are
 // visible; nothing that step writes is read before it.  The filter issues its score loads (input
 // only) before the wait, beside the sample step.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // bitonic sort of one value per thread over a 1024-thread block, descending (thread t ends with
 // sorted position t); partners closer than a warp exchange by shuffles, the others through
