@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t split_pair(float2 x, uint32_t& mid, uint32_t
 }
 
 __device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
-// the same by the FMA pipe for the first POLY of every four pairs (Q: the pair)
+// the same by the FMA pipe for the first POLY of every four pairs (Q: the pair), which takes NaN for a small exponent
 template <int Q, int POLY>
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
   if constexpr ((Q & 3) < POLY) return exp2_poly2(x);
@@ -751,6 +751,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ WeightBars<NST> bars;
   __shared__ float half_sum[kRows];
+  __shared__ int last_nan;   // the last row whose offset is NaN: the keys that it sees get one whichever unit made their exponentials
   __shared__ uint32_t tmem_base;
   __shared__ PromptTile item;
   __shared__ int abort_word;
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
   float total = 0.0f;
 
   if (warp == kProducer) {
-    int issued = 0;
+    int issued = 0, nan_row = INT32_MIN;
     const float* offset = p.offset + static_cast<int64_t>(h) * a.total_q + qr.first;
     for (int t = 0; t < NT; ++t) {
       const int s = t % NST, i0 = (rt0 + t) * kRows;
@@ -837,6 +838,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        if (isnan(v[k])) nan_row = i0 + lane + 32 * k;
         const uint32_t hi = pack_bf16x2(v[k], 0.0f);
         const float r1 = v[k] - __uint_as_float(hi << 16);
         const uint32_t mid = pack_bf16x2(r1, 0.0f);
@@ -849,7 +851,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
       mbar_arrive(&bars.q_full[s]);
       ++issued;
     }
-    __syncwarp();
+    nan_row = __reduce_max_sync(0xffffffffu, nan_row);
+    if (lane == 0) last_nan = nan_row;
     if (lane == 0 && NT > 0) {   // as in the output kernel
       drain_wait(&bars.k_full, 0);
       for (int x = max(0, issued - NST); x < issued; ++x) drain_wait(&bars.q_full[x % NST], (x / NST) & 1);
@@ -943,8 +946,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
   const bool any_abort = __syncthreads_or(aborted);
   if (any_abort && tid == 0) report(a.dev_status, SPATTEN_E_TIMEOUT);
   if (tid < kRows && j0 + tid < kr.n) {
-    const float sum = any_abort ? 0.0f : total + half_sum[tid];
     const int j = j0 + tid;
+    const float sum = any_abort ? 0.0f : (last_nan >= j - shift ? NAN : total + half_sum[tid]);
     if (G > 1) {
       p.part[static_cast<int64_t>(h) * a.total_kv + kr.first + j] = sum;
     } else if (j < a.weight_cap) {

@@ -372,7 +372,8 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  *    nothing and are not written.  Offsets that decrease or leave [0, total] are reported (SPATTEN_E_INDEX) and
  *    their sequence is taken as empty.
  *  - Infinities and NaN in rows of other sequences, or outside every sequence, change nothing.  Inside
- *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable.
+ *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable; a NaN in a
+ *    query row makes its output, and the weights of the keys that it sees, NaN.
  *  - weight rows j >= weight_cap are not written and reported (SPATTEN_E_INDEX).
  *  - o overlaps none of the inputs.
  *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
