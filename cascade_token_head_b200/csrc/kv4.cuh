@@ -26,17 +26,42 @@ __device__ __forceinline__ PackedRows packed_rows(const int32_t* cu, int b, int 
   return {s, e - s, false};
 }
 
-// The sequence that owns packed row r: the last b with cu[b] <= r (B sequences; -1: none).
-__device__ __forceinline__ int owner_of_row(const int32_t* cu, int B, int r) {
-  if (!cu) return r < B ? r : -1;
-  int lo = 0, hi = B;   // cu[lo] <= r < cu[hi] is the invariant sought
-  if (r < cu[0] || r >= cu[B]) return -1;
+// The first sequence that packed row r belongs to (-1: none), by the whole warp: each sequence is asked, so that
+// one with bad offsets hides no other.
+__device__ __forceinline__ int owner_of_row(const int32_t* cu, int B, int total, int r) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const PackedRows p = b0 + lane < B ? packed_rows(cu, b0 + lane, total) : PackedRows{0, 0, false};
+    const uint32_t in = __ballot_sync(0xffffffffu, r >= p.first && r - p.first < p.n);
+    if (in) return b0 + __ffs(in) - 1;
+  }
+  return -1;
+}
+// The same for a row of each lane's own (rows past total have none).  A binary search finds it where offsets do
+// not decrease; rows that it does not find are looked for one by one if a sequence has bad offsets.
+__device__ __forceinline__ int owner_of_lanes_row(const int32_t* cu, int B, int total, int r) {
+  int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] <= r) lo = mid;
     else hi = mid;
   }
-  return lo;
+  const PackedRows p = packed_rows(cu, lo, total);
+  const bool found = r >= p.first && r - p.first < p.n;
+  uint32_t missing = __ballot_sync(0xffffffffu, !found && r < total);
+  int b = found ? lo : -1;
+  if (!missing) return b;
+  bool bad = false;
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < B; i += 32) bad |= packed_rows(cu, i, total).bad;
+  if (!__any_sync(0xffffffffu, bad)) return b;
+#pragma unroll 1
+  for (; missing; missing &= missing - 1) {
+    const int lane = __ffs(missing) - 1, owner = owner_of_row(cu, B, total, __shfl_sync(0xffffffffu, r, lane));
+    if (lane == (threadIdx.x & 31)) b = owner;
+  }
+  return b;
 }
 
 // The sequence and tile number t, for tiles of `rows` packed rows that start anew at each sequence:

@@ -68,12 +68,9 @@ __global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem
   grid_dep_wait();
   const spatten_prompt_args& a = p.a;
   const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
-  if (r >= a.total_kv) return;
-  const int b = owner_of_row(a.cu_kv, a.B, r);
+  const int b = owner_of_lanes_row(a.cu_kv, a.B, a.total_kv, r);
   if (b < 0) return;
-  const PackedRows kr = packed_rows(a.cu_kv, b, a.total_kv);
-  const int j = r - kr.first;
-  if (kr.bad || j < 0 || j >= kr.n) return;
+  const int j = r - a.cu_kv[b];
   if (j >= a.weight_cap) {
     report(a.dev_status, SPATTEN_E_INDEX);
     return;

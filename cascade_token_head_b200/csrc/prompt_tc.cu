@@ -670,33 +670,38 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptProblem p) {
   grid_dep_trigger();
   grid_dep_wait();
   const spatten_prompt_args& a = p.a;
-  constexpr int N = DH / 32;
+  constexpr int N = DH / 32, kInFlight = 8;
+  static_assert(kMaxSplits % kInFlight == 0, "whole rounds");
   const int lane = threadIdx.x & 31;
   const int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int row = static_cast<int>(x / a.H), h = static_cast<int>(x % a.H);
   if (row >= a.total_q) return;
-  const int b = owner_of_row(a.cu_q, a.B, row);
-  if (b < 0) return;
-  const PackedRows qr = packed_rows(a.cu_q, b, a.total_q);
-  if (qr.bad || row < qr.first || row - qr.first >= qr.n) return;   // rows of no sequence stay as they are
   const int64_t at = static_cast<int64_t>(h) * a.total_q + row, step = static_cast<int64_t>(a.H) * a.total_q;
   static_assert(kMaxSplits <= 32, "a lane a split");
   const float2 ml = lane < p.splits ? p.split_ml[lane * step + at] : make_float2(-INFINITY, 0.0f);
+  if (owner_of_row(a.cu_q, a.B, a.total_q, row) < 0) return;   // rows of no sequence stay as they are (and have no parts)
   float m = ml.x;
 #pragma unroll
   for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   // a split without keys has l = 0 and left no output; a NaN goes on
   const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - (m == -INFINITY ? 0.0f : m));
   float l = 0.0f, o[N] = {};
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const float ls = __shfl_sync(0xffffffffu, ml.y, s), fs = __shfl_sync(0xffffffffu, f, s);
-    const float* part = p.split_o + (s * step + at) * DH + lane * N;
-    l = fmaf(ls, fs, l);
+  for (int s0 = 0; s0 < p.splits; s0 += kInFlight) {
+    float v[kInFlight][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float v = ls == 0.0f ? 0.0f : part[i];
-      o[i] = fmaf(v, fs, o[i]);
+    for (int u = 0; u < kInFlight; ++u) {   // of a split that left no output too: that is read and not used
+      const float* part = p.split_o + (min(s0 + u, p.splits - 1) * step + at) * DH + lane * N;
+      if constexpr (N == 4)
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[u][0]), "=f"(v[u][1]), "=f"(v[u][N - 2]), "=f"(v[u][N - 1]) : "l"(part));
+      else
+        asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[u][0]), "=f"(v[u][1]) : "l"(part));
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {   // splits past the last: lanes of l = 0
+      const float ls = __shfl_sync(0xffffffffu, ml.y, s0 + u), fs = __shfl_sync(0xffffffffu, f, s0 + u);
+      l = fmaf(ls, fs, l);
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = fmaf(ls == 0.0f ? 0.0f : v[u][i], fs, o[i]);
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);

@@ -370,7 +370,7 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  * values do), float32 for float32 ones; statistics and sums are float32.
  *  - total_q and total_kv are the rows of the packed blocks; rows outside every sequence change
  *    nothing and are not written.  Offsets that decrease or leave [0, total] are reported (SPATTEN_E_INDEX) and
- *    their sequence is taken as empty.
+ *    their sequence is taken as empty; where other sequences then overlap, their results are unspecified.
  *  - Infinities and NaN in rows of other sequences, or outside every sequence, change nothing.  Inside
  *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable; a NaN in a
  *    query row makes its output, and the weights of the keys that it sees, NaN.

@@ -35,3 +35,40 @@ def test_prompt_nonfinite_query_row(cuda, kernel, dtype, d, n_q, n_kv, row, valu
     check_out(o, ref, spread, e, dtype, UBF if dtype == BF and kernel == 0 else 0.0)
     check_weight(got[0, 0, seen:], host(p.w0)[0, 0, seen:], w[0, 0, seen:], e)
     check_weight(got[0, 1], host(p.w0)[0, 1], w[0, 1], e)
+
+
+OUTSIDE = 10 ** 6   # an offset that leaves the block
+MANY = [5 * b for b in range(41)]
+MANY[20] = OUTSIDE
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("cu_q,cu_kv", [
+    ([30, 20, 50], [30, 20, 50]), ([0, 40, 100, 60], [0, 40, 100, 60]), ([0, 5, OUTSIDE, 5, 100], [0, 5, OUTSIDE, 5, 100]),
+    ([7, 7, 2, 9], [0, 3000, 3000, 7000]), ([0, 3, 6, 4], [0, 4000, 8000, 8000]),
+    ([0, 3, 9], [4000, 3000, 9000]), ([0, 5, -1, 5, 8], [0, 2000, 4000, 4000, 8000]), (MANY, MANY)])
+def test_prompt_sound_sequences_next_to_bad_offsets(cuda, dtype, H, Hk, cu_q, cu_kv):
+    """Offsets that decrease or leave their block make their own sequence empty; the others are whole, with
+    grouped heads (whose weights a kernel of their own adds up) and with keys split over CTAs too."""
+    S, B, d = lib(), len(cu_q) - 1, 64
+    top = lambda cu: max(c for c in cu if c != OUTSIDE)
+    q_rows, kv_rows = top(cu_q), top(cu_kv)
+    p = Prompt(S, dtype, d, H, Hk, [q_rows] + [0] * (B - 1), [kv_rows] + [0] * (B - 1), seed=B + H)
+    cq, ck = i32(cu_q), i32(cu_kv)
+    p.args.cu_q, p.args.cu_kv = cq.data_ptr(), ck.data_ptr()
+    p.run()
+    assert int(p.status.item()) == S.E_INDEX
+    rows = lambda cu, n, b: (cu[b], cu[b + 1]) if 0 <= cu[b] <= cu[b + 1] <= n else (0, 0)
+    q, k, v, o = host(p.q), host(p.k), host(p.v), host(p.o)
+    rest = np.ones(q_rows, bool)
+    for b in range(B):
+        q0, q1 = rows(cu_q, q_rows, b)
+        k0, k1 = rows(cu_kv, kv_rows, b)
+        one = lambda v: R.prompt_attention(q[q0:q1], k[k0:k1], v, [0, q1 - q0], [0, k1 - k0], p.n_w)
+        (ref, w), (spread, _) = one(v[k0:k1]), one(np.abs(v[k0:k1]))
+        e = score_step(q[q0:q1], k[k0:k1], k1 - k0)
+        check_out(o[q0:q1], ref, spread, e, dtype, UBF if dtype == BF else 0.0, f"sequence {b}")
+        check_weight(host(p.w)[b], host(p.w0)[b], w[0], e, f"sequence {b}")
+        rest[q0:q1] = False
+    assert (o[rest] == 7.0).all(), "rows outside every sequence were written"
