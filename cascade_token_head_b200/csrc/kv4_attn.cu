@@ -424,18 +424,29 @@ struct Warp {
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh) {
         float p[4] = {s[nh][0] * f0, s[nh][1] * f0, s[nh][2] * f1, s[nh][3] * f1};
-#pragma unroll
-        for (int e = 0; e < kP; ++e) {
-          const uint32_t u0 = pack_bf16(p[0], p[1]), u1 = pack_bf16(p[2], p[3]);
-          if (e + 1 < kP) {
-            p[0] -= bf_lo(u0);
-            p[1] -= bf_hi(u0);
-            p[2] -= bf_lo(u1);
-            p[3] -= bf_hi(u1);
-          }
-          const uint32_t b0 = transpose8x8(u0), b1 = transpose8x8(u1);
+        if constexpr (kP == 1) {
+          const uint32_t b0 = transpose8x8(pack_bf16(p[0], p[1])), b1 = transpose8x8(pack_bf16(p[2], p[3]));
           mma_bf16(o[nh][2 * j], av[0], b0, b1);
           mma_bf16(o[nh][2 * j + 1], av[1], b0, b1);
+        } else {
+          // The tensor cores cut their sums off: over a long run these would drift towards 0.  Sixteen keys start from
+          // 0, small terms first, and are added here, rounded to nearest.
+          uint32_t b[kP][2];
+#pragma unroll
+          for (int e = 0; e < kP; ++e) {
+            const uint32_t u0 = pack_bf16(p[0], p[1]), u1 = pack_bf16(p[2], p[3]);
+            p[0] -= bf_lo(u0), p[1] -= bf_hi(u0), p[2] -= bf_lo(u1), p[3] -= bf_hi(u1);
+            b[e][0] = transpose8x8(u0), b[e][1] = transpose8x8(u1);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float t16[4];
+            mma_bf16_zero(t16, av[c], b[kP - 1][0], b[kP - 1][1]);
+#pragma unroll
+            for (int e = kP - 2; e >= 0; --e) mma_bf16(t16, av[c], b[e][0], b[e][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nh][2 * j + c][k] += t16[k];
+          }
         }
       }
     }

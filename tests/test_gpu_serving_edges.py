@@ -72,3 +72,37 @@ def test_prompt_sound_sequences_next_to_bad_offsets(cuda, dtype, H, Hk, cu_q, cu
         check_weight(host(p.w)[b], host(p.w0)[b], w[0], e, f"sequence {b}")
         rest[q0:q1] = False
     assert (o[rest] == 7.0).all(), "rows outside every sequence were written"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [1, 40])
+def test_attention_float32_sums_do_not_drift(cuda, d, B):
+    """Float32 queries over 16,000 rows, values of one sign: sums that cut their last bits off fall short by a part
+    that grows with the rows (kept in the tensor cores over a whole sequence, 1.6e-6; over an eighth of it, 5.4e-7).
+    One sequence, and so many that one CTA sums most of a sequence (all have the same rows and queries of their
+    own).  The scores are below 4 and each output is a mean of about n values with independent errors: rounded
+    to nearest they are 2**-22 or so each (scores, exponentials), and their mean over all outputs is far below
+    that: 2**-21 is left for it, and 2**-19 for a single output."""
+    S, Hk, n = lib(), 8, 16000
+    r = np.random.default_rng(d)
+    codes = [r.integers(-7, 8, (n, d)), r.integers(1, 8, (n, d))]
+    scales = [R.to_bf16(np.exp(r.normal(0, 0.3, (n, d // 32)))) for _ in range(2)]
+    dev = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda().expand(B, Hk, *a.shape).contiguous()
+    t = [dev(R.pack4(codes[0], 8), torch.uint8), dev(scales[0], BF), dev(R.pack4(codes[1], 4), torch.uint8), dev(scales[1], BF)]
+    w = torch.zeros((B, Hk, n), device="cuda")
+    c = S.make_kv4_cache(*t, w)
+    k, v = (a * np.repeat(s.astype(np.float64), 32, -1) for a, s in zip(codes, scales))
+    q = torch.randn((B, Hk, d), generator=torch.Generator(device="cuda").manual_seed(d), device="cuda") * 0.08
+    o, status = torch.empty_like(q), i32([0])
+    a = S.make_kv4_attn_args(c, q, o, i32([n] * B), n, dev_status=status)
+    nb = S.kv4_attention_workspace_size(a)
+    S.kv4_attention(a, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    qh = host(q).reshape(-1, d)
+    x = qh @ k.T / np.sqrt(d)
+    assert np.abs(x).max() < 4
+    p = R.softmax_rows(x)
+    ref = p @ v
+    rel = host(o).reshape(-1, d) / ref - 1
+    assert int(status.item()) == 0
+    assert abs(rel.mean()) <= 2.0 ** -21 and np.abs(rel).max() <= 2.0 ** -19
+    assert abs(host(w).sum() / p.sum() - 1) <= 2.0 ** -21
