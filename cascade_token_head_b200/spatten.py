@@ -358,6 +358,7 @@ def prompt_workspace_size(args: prompt_args) -> int:
 
 
 def prompt_attention(args: prompt_args, ws=None, ws_bytes: int = 0, stream=None):
+    _check_device(args._device, ws)
     _run(lib.spatten_prompt_attention, "spatten_prompt_attention", args._device, stream, C.byref(args), ptr(ws), ws_bytes)
 
 
@@ -383,14 +384,14 @@ _append_fn, _read_fn = lib.spatten_kv4_append, lib.spatten_kv4_read
 def kv4_append(cache: kv4_cache, k, v, ld_tok, total, len, len_out, seen=None, seen_out=None, cu=None, dtype=None,
                dev_status=None, stream=None):
     dt = dtype_code(k) if dtype is None else dtype
-    _check_device(cache._device, k, v, len, len_out, cu)
+    _check_device(cache._device, k, v, len, len_out, seen, seen_out, cu, dev_status)
     _run(_append_fn, "spatten_kv4_append", cache._device, stream, cache._ref, ptr(k), ptr(v), dt, ld_tok, total, ptr(cu), ptr(len),
          ptr(len_out), ptr(seen), ptr(seen_out), ptr(dev_status))
 
 
 def kv4_read(cache: kv4_cache, cu, total, k_out, v_out, ld_tok, row0=None, dtype=None, dev_status=None, stream=None):
     dt = dtype_code(k_out if k_out is not None else v_out) if dtype is None else dtype
-    _check_device(cache._device, cu, k_out, v_out)
+    _check_device(cache._device, cu, k_out, v_out, row0, dev_status)
     _run(_read_fn, "spatten_kv4_read", cache._device, stream, cache._ref, ptr(cu), ptr(row0), total, ptr(k_out), ptr(v_out), dt,
          ld_tok, ptr(dev_status))
 
@@ -420,6 +421,7 @@ def kv4_attention_workspace_size(args: kv4_attn_args) -> int:
 
 
 def kv4_attention(args: kv4_attn_args, ws, ws_bytes: int, stream=None):
+    _check_device(args._device, ws)
     _run(lib.spatten_kv4_attention, "spatten_kv4_attention", args._device, stream, C.byref(args), ptr(ws), ws_bytes)
 
 
@@ -429,6 +431,8 @@ def kv4_evict_workspace_size(cache: kv4_cache, n_max: int, keep: int) -> int:
 
 def kv4_evict(src: kv4_cache, dst: kv4_cache, len, len_out, seen, n_max, keep, recent, ws, ws_bytes: int,
               dev_status=None, stream=None):
-    _check_device(src._device, dst._keep[0], len, len_out, ws)
+    if dst._device != src._device:
+        raise ValueError("the tensors of a call are on one device")
+    _check_device(src._device, len, len_out, seen, ws, dev_status)
     _run(lib.spatten_kv4_evict, "spatten_kv4_evict", src._device, stream, src._ref, dst._ref, ptr(len), ptr(len_out), ptr(seen),
          n_max, keep, recent, ptr(ws), ws_bytes, ptr(dev_status))
