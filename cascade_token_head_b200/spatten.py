@@ -285,6 +285,22 @@ def _check_device(device, *tensors):
             raise ValueError("the tensors of a call are on one device")
 
 
+_int32 = None   # torch.int32, set with the first cache (a lookup in `torch` costs 0.1 us a call)
+
+
+def _vector(t, n, device):
+    """Address of a vector of n counts, positions or offsets on `device` (None and addresses pass through)."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not _int32 or not t.is_contiguous():
+        raise TypeError("counts, positions, offsets and status words are contiguous int32 vectors")
+    if t.numel() != n:
+        raise ValueError(f"a vector has {t.numel()} entries where the call reads {n}")
+    if t.get_device() != device:
+        raise ValueError("the tensors of a call are on one device")
+    return t.data_ptr()
+
+
 _get_device = None
 
 
@@ -365,7 +381,9 @@ def prompt_attention(args: prompt_args, ws=None, ws_bytes: int = 0, stream=None)
 def make_kv4_cache(k_codes, k_scale, v_codes, v_scale, weight=None, pos=None) -> kv4_cache:
     """The description of a 4-bit cache from its tensors: codes uint8 [B, H_kv, cap, d_h / 2], scales
     bfloat16 [B, H_kv, cap, d_h / 32], weight float32 and pos int32 [B, H_kv, cap] (all contiguous)."""
+    global _int32
     import torch
+    _int32 = torch.int32
     B, H, cap, half = k_codes.shape
     want = [(k_codes, torch.uint8, (half,)), (v_codes, torch.uint8, (half,)), (k_scale, torch.bfloat16, (half // 16,)),
             (v_scale, torch.bfloat16, (half // 16,)), (weight, torch.float32, ()), (pos, torch.int32, ())]
@@ -384,16 +402,19 @@ _append_fn, _read_fn = lib.spatten_kv4_append, lib.spatten_kv4_read
 def kv4_append(cache: kv4_cache, k, v, ld_tok, total, len, len_out, seen=None, seen_out=None, cu=None, dtype=None,
                dev_status=None, stream=None):
     dt = dtype_code(k) if dtype is None else dtype
-    _check_device(cache._device, k, v, len, len_out, seen, seen_out, cu, dev_status)
-    _run(_append_fn, "spatten_kv4_append", cache._device, stream, cache._ref, ptr(k), ptr(v), dt, ld_tok, total, ptr(cu), ptr(len),
-         ptr(len_out), ptr(seen), ptr(seen_out), ptr(dev_status))
+    device, B = cache._device, cache.B
+    _check_device(device, k, v)
+    _run(_append_fn, "spatten_kv4_append", device, stream, cache._ref, ptr(k), ptr(v), dt, ld_tok, total, _vector(cu, B + 1, device),
+         _vector(len, B, device), _vector(len_out, B, device), _vector(seen, B, device), _vector(seen_out, B, device),
+         _vector(dev_status, 1, device))
 
 
 def kv4_read(cache: kv4_cache, cu, total, k_out, v_out, ld_tok, row0=None, dtype=None, dev_status=None, stream=None):
     dt = dtype_code(k_out if k_out is not None else v_out) if dtype is None else dtype
-    _check_device(cache._device, cu, k_out, v_out, row0, dev_status)
-    _run(_read_fn, "spatten_kv4_read", cache._device, stream, cache._ref, ptr(cu), ptr(row0), total, ptr(k_out), ptr(v_out), dt,
-         ld_tok, ptr(dev_status))
+    device, B = cache._device, cache.B
+    _check_device(device, k_out, v_out)
+    _run(_read_fn, "spatten_kv4_read", device, stream, cache._ref, _vector(cu, B + 1, device), _vector(row0, B, device), total,
+         ptr(k_out), ptr(v_out), dt, ld_tok, _vector(dev_status, 1, device))
 
 
 def make_kv4_attn_args(cache: kv4_cache, q, o, len, n_max, update_weight=True, sm_scale=0.0,
@@ -431,8 +452,9 @@ def kv4_evict_workspace_size(cache: kv4_cache, n_max: int, keep: int) -> int:
 
 def kv4_evict(src: kv4_cache, dst: kv4_cache, len, len_out, seen, n_max, keep, recent, ws, ws_bytes: int,
               dev_status=None, stream=None):
-    if dst._device != src._device:
+    device, B = src._device, src.B
+    if dst._device != device:
         raise ValueError("the tensors of a call are on one device")
-    _check_device(src._device, len, len_out, seen, ws, dev_status)
-    _run(lib.spatten_kv4_evict, "spatten_kv4_evict", src._device, stream, src._ref, dst._ref, ptr(len), ptr(len_out), ptr(seen),
-         n_max, keep, recent, ptr(ws), ws_bytes, ptr(dev_status))
+    _check_device(device, ws)
+    _run(lib.spatten_kv4_evict, "spatten_kv4_evict", device, stream, src._ref, dst._ref, _vector(len, B, device),
+         _vector(len_out, B, device), _vector(seen, B, device), n_max, keep, recent, ptr(ws), ws_bytes, _vector(dev_status, 1, device))

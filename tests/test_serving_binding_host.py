@@ -84,3 +84,25 @@ def test_eviction_into_a_cache_elsewhere_is_refused(S):
     with pytest.raises(ValueError, match="one device"):
         S.kv4_evict(src, dst, i32(0, 0), i32(0, 0), i32(0, 0), CAP, 4, 1, zeros(1 << 16, dt=torch.uint8), 1 << 16)
     assert not S.calls
+
+
+@pytest.mark.parametrize("op", ["append", "read", "evict"])
+def test_counts_and_offsets_are_int32_vectors_of_their_length(S, op):
+    """What a kernel reads as B (offsets: B + 1) 32-bit words is that: not int64, not one entry less, not strided."""
+    call, args = calls(S)[op]
+    for name, t in args.items():
+        if t.dtype != torch.int32:
+            continue
+        n = 1 if name == "dev_status" else (B + 1 if name == "cu" else B)
+        with pytest.raises(TypeError):
+            call(**dict(args, **{name: zeros(n, dt=torch.int64)}))
+        with pytest.raises(TypeError):
+            call(**dict(args, **{name: zeros(n)}))
+        if n > 1:
+            with pytest.raises(TypeError):
+                call(**dict(args, **{name: zeros(n, 2, dt=torch.int32)[:, 0]}))
+        with pytest.raises(ValueError):
+            call(**dict(args, **{name: zeros(n - 1, dt=torch.int32)}))
+        with pytest.raises(ValueError):
+            call(**dict(args, **{name: zeros(n + 1, dt=torch.int32)}))
+    assert not S.calls
