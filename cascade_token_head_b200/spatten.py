@@ -285,6 +285,21 @@ def _check_device(device, *tensors):
             raise ValueError("the tensors of a call are on one device")
 
 
+def _rows_dtype(device, dtype, *tensors) -> int:
+    """The dtype code that a call's row blocks, all on `device`, have (addresses are not looked at)."""
+    for t in tensors:
+        if t is None or type(t) is int:
+            continue
+        if t.get_device() != device:
+            raise ValueError("the tensors of a call are on one device")
+        code = dtype_code(t)
+        if dtype is None:
+            dtype = code
+        elif dtype != code:
+            raise TypeError("the rows of a call have one dtype")
+    return dtype
+
+
 _int32 = None   # torch.int32, set with the first cache (a lookup in `torch` costs 0.1 us a call)
 
 
@@ -401,18 +416,16 @@ _append_fn, _read_fn = lib.spatten_kv4_append, lib.spatten_kv4_read
 
 def kv4_append(cache: kv4_cache, k, v, ld_tok, total, len, len_out, seen=None, seen_out=None, cu=None, dtype=None,
                dev_status=None, stream=None):
-    dt = dtype_code(k) if dtype is None else dtype
     device, B = cache._device, cache.B
-    _check_device(device, k, v)
+    dt = _rows_dtype(device, dtype, k, v)
     _run(_append_fn, "spatten_kv4_append", device, stream, cache._ref, ptr(k), ptr(v), dt, ld_tok, total, _vector(cu, B + 1, device),
          _vector(len, B, device), _vector(len_out, B, device), _vector(seen, B, device), _vector(seen_out, B, device),
          _vector(dev_status, 1, device))
 
 
 def kv4_read(cache: kv4_cache, cu, total, k_out, v_out, ld_tok, row0=None, dtype=None, dev_status=None, stream=None):
-    dt = dtype_code(k_out if k_out is not None else v_out) if dtype is None else dtype
     device, B = cache._device, cache.B
-    _check_device(device, k_out, v_out)
+    dt = _rows_dtype(device, dtype, k_out, v_out)
     _run(_read_fn, "spatten_kv4_read", device, stream, cache._ref, _vector(cu, B + 1, device), _vector(row0, B, device), total,
          ptr(k_out), ptr(v_out), dt, ld_tok, _vector(dev_status, 1, device))
 

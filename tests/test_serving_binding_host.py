@@ -106,3 +106,19 @@ def test_counts_and_offsets_are_int32_vectors_of_their_length(S, op):
         with pytest.raises(ValueError):
             call(**dict(args, **{name: zeros(n + 1, dt=torch.int32)}))
     assert not S.calls
+
+
+@pytest.mark.parametrize("op,names", [("append", ("k", "v")), ("read", ("k_out", "v_out"))])
+def test_row_blocks_of_two_dtypes_are_refused(S, op, names):
+    """The wider type's reads or writes would leave the other block."""
+    call, args = calls(S)[op]
+    for name in names:
+        with pytest.raises(TypeError):
+            call(**dict(args, **{name: zeros(5, HK, D, dt=torch.bfloat16)}))
+        with pytest.raises(TypeError):
+            call(**dict(args, **{name: zeros(5, HK, D, dt=torch.float16)}))
+    with pytest.raises(TypeError):
+        call(dtype=S.BF16, **args)
+    assert not S.calls
+    call(dtype=S.F32, **args)
+    assert len(S.calls) == 1
