@@ -11,6 +11,8 @@ that use them (``spatten_prompt_attention``, ``spatten_kv4_append`` / ``_attenti
 Calls run on the state's GPU, on torch's current stream there.  The counts live on the device, so ``step`` and ``evict`` can be
 captured in a CUDA graph and replayed.
 """
+import ctypes as C
+
 import torch
 
 from . import spatten as S
@@ -24,6 +26,8 @@ class KV4State:
     (next position), ``status`` (first device-side error, 0 = none)."""
 
     def __init__(self, B, H, H_kv, d_h, cap, device="cuda"):
+        if not 1 <= H <= 1024 or H_kv < 1 or H % H_kv or d_h not in (64, 128):
+            raise ValueError("H is a multiple of H_kv, up to 1024, and d_h 64 or 128")
         self.B, self.H, self.H_kv, self.d_h, self.cap = B, H, H_kv, d_h, cap
         z = lambda *shape, dt: torch.zeros(shape, dtype=dt, device=device)
         self.k_codes, self.v_codes = (z(B, H_kv, cap, d_h // 2, dt=torch.uint8) for _ in range(2))
@@ -59,38 +63,57 @@ class KV4State:
     def prompt(self, q, k, v, cu, o=None):
         """Causal attention of packed prompts (rows cu[b] .. cu[b+1]-1 are sequence b's) into an empty
         cache: returns the outputs, appends the rows and adds their attention weights."""
+        o, *call = self._prepare(q, k, v, cu, None, o)
         self.append(k, v, cu)
-        return self._attention(q, k, v, cu, None, o)
+        S.prompt_attention(*call)
+        return o
 
     def resume(self, q, k, v, cu, cu_kv, rows, o=None):
         """Packed prompts that go on over the cached rows.  cu_kv [B + 1] are the offsets of each
         sequence's cached and new rows together, ``rows`` their number in all.  Every row, the new ones
         too, takes part as the value its codes stand for."""
-        self.append(k, v, cu)
+        if cu_kv is None:
+            raise ValueError("cu_kv has the offsets of each sequence's cached and new rows together")
         kk, vv = (torch.zeros((rows, self.H_kv, self.d_h), dtype=q.dtype, device=q.device) for _ in range(2))
+        o, *call = self._prepare(q, kk, vv, cu, cu_kv, o)
+        self.append(k, v, cu)
         S.kv4_read(self.cache, cu_kv, rows, kk, vv, self.H_kv * self.d_h, dev_status=self.status)
-        return self._attention(q, kk, vv, cu, cu_kv, o)
+        S.prompt_attention(*call)
+        return o
 
-    def _attention(self, q, k, v, cu, cu_kv, o):
+    def _prepare(self, q, k, v, cu, cu_kv, o):
+        """A prompt's outputs, arguments and workspace.  What the call would refuse is refused here, before its
+        rows are appended."""
         o = torch.empty_like(q) if o is None else o
         a = S.make_prompt_args(q, k, v, o, cu, cu_kv, weight=self.weight, dev_status=self.status)
+        # made without its workspace, which one with weights needs and which is looked at last, it launches nothing
+        status = S.lib.spatten_prompt_attention(C.byref(a), None, 0, None)
+        if status != S.E_WORKSPACE:
+            S.check(status, "spatten_prompt_attention")
         nb = S.prompt_workspace_size(a)
-        S.prompt_attention(a, self._workspace("prompt", nb), nb)
-        return o
+        return o, a, self._workspace("prompt", nb), nb
 
     def attend(self, q, o=None, n_max=None, update_weight=True):
         """Attention of one query row per sequence, q [B, H, d_h], over the cached rows."""
-        o = torch.empty_like(q) if o is None else o
-        a = S.make_kv4_attn_args(self.cache, q, o, self.len, self.cap if n_max is None else n_max, update_weight,
-                                 dev_status=self.status)
-        nb = S.kv4_attention_workspace_size(a)
-        S.kv4_attention(a, self._workspace("attend", nb), nb)
+        o, *call = self._prepare_row(q, o, n_max, update_weight)
+        S.kv4_attention(*call)
         return o
 
     def step(self, q, k, v, o=None, n_max=None):
         """One token per sequence: append its key and value rows [B, H_kv, d_h], then attend."""
+        o, *call = self._prepare_row(q, o, n_max, True)
         self.append(k, v)
-        return self.attend(q, o, n_max)
+        S.kv4_attention(*call)
+        return o
+
+    def _prepare_row(self, q, o, n_max, update_weight):
+        o = torch.empty_like(q) if o is None else o
+        a = S.make_kv4_attn_args(self.cache, q, o, self.len, self.cap if n_max is None else n_max, update_weight,
+                                 dev_status=self.status)
+        nb = S.kv4_attention_workspace_size(a)
+        if nb == 0:   # the call says what is wrong with it
+            S.check(S.lib.spatten_kv4_attention(C.byref(a), None, 0, None), "spatten_kv4_attention")
+        return o, a, self._workspace("attend", nb), nb
 
     def evict(self, keep, recent=0, n_max=None):
         """Keep each head's ``keep`` rows with the most accumulated weight (and the last ``recent``)."""
