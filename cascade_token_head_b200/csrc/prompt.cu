@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(256) prompt_weight_reduce_kernel(PromptProblem
   const int r = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y, G = a.H / a.H_kv;
   const int b = owner_of_lanes_row(a.cu_kv, a.B, a.total_kv, r);
   if (b < 0) return;
-  const int j = r - a.cu_kv[b];
+  const int first = a.cu_kv[b], j = r - first;
+  if (!counts_rows(a, b, a.cu_kv[b + 1] - first)) return;
   if (j >= a.weight_cap) {
     report(a.dev_status, SPATTEN_E_INDEX);
     return;

@@ -84,11 +84,18 @@ __device__ __forceinline__ PromptTile find_prompt_tile(const spatten_prompt_args
   return r;
 }
 
-// Reports offsets that decrease or leave their block (one block of a call does it).
+// Whether the n_kv keys of sequence b are the rows that its weights count.
+__device__ __forceinline__ bool counts_rows(const spatten_prompt_args& a, int b, int n_kv) {
+  return !a.weight_len || a.weight_len[b] == min(n_kv, a.weight_cap);
+}
+
+// Reports offsets that decrease or leave their block, and keys that are not the weights' rows (one block of a
+// call does it).
 __device__ __forceinline__ void report_bad_offsets(const spatten_prompt_args& a) {
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x)
-    if (packed_rows(a.cu_q, b, a.total_q).bad || packed_rows(a.cu_kv, b, a.total_kv).bad)
-      report(a.dev_status, SPATTEN_E_INDEX);
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const PackedRows q = packed_rows(a.cu_q, b, a.total_q), k = packed_rows(a.cu_kv, b, a.total_kv);
+    if (q.bad || k.bad || (a.weight && q.n > 0 && !counts_rows(a, b, k.n))) report(a.dev_status, SPATTEN_E_INDEX);
+  }
 }
 
 int32_t prompt_simt_launch(const PromptProblem& p, cudaStream_t st);

@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) prompt_weight_simt_kernel(PromptProb
   if (st.b < 0) return;
   const PackedRows qr = packed_rows(a.cu_q, st.b, a.total_q), kr = packed_rows(a.cu_kv, st.b, a.total_kv);
   const int j0 = st.tile * kTile, shift = kr.n - qr.n;
+  const bool counted = counts_rows(a, st.b, kr.n);
   load_channels<DH, T>(sm.k, a.k, a.kv_ld_tok, hk, static_cast<int64_t>(kr.first) + j0, min(kTile, kr.n - j0));
   const float scale = a.sm_scale * kLog2e;
   const float2* stats = p.stats + static_cast<int64_t>(h) * a.total_q + qr.first;
@@ -217,6 +218,8 @@ __global__ void __launch_bounds__(kThreads) prompt_weight_simt_kernel(PromptProb
   for (int y = 0; y < 16; ++y) t += sm.p[j][y];
   if (G > 1)
     p.part[static_cast<int64_t>(h) * a.total_kv + kr.first + j0 + j] = t;
+  else if (!counted)
+    return;
   else if (j0 + j < a.weight_cap)
     a.weight[static_cast<int64_t>(st.b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j0 + j] += t;
   else

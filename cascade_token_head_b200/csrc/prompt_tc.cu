@@ -817,6 +817,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
   }
   const PackedRows qr = pt.q, kr = pt.k;
   const int j0 = pt.tile * kRows, shift = kr.n - qr.n;
+  const bool counted = counts_rows(a, pt.b, kr.n);
   const int rt0 = first_tile(pt), NT = max(0, (qr.n + kRows - 1) / kRows - rt0);
   bool aborted = false;
   float total = 0.0f;
@@ -955,6 +956,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_weight_kernel(Pr
     const float sum = any_abort ? 0.0f : (last_nan >= j - shift ? NAN : total + half_sum[tid]);
     if (G > 1) {
       p.part[static_cast<int64_t>(h) * a.total_kv + kr.first + j] = sum;
+    } else if (!counted) {   // reported by the output kernel
     } else if (j < a.weight_cap) {
       a.weight[static_cast<int64_t>(pt.b) * a.weight_ld_seq + static_cast<int64_t>(hk) * a.weight_ld_head + j] += sum;
     } else {

@@ -62,7 +62,8 @@ class KV4State:
 
     def prompt(self, q, k, v, cu, o=None):
         """Causal attention of packed prompts (rows cu[b] .. cu[b+1]-1 are sequence b's) into an empty
-        cache: returns the outputs, appends the rows and adds their attention weights."""
+        cache: returns the outputs, appends the rows and adds their attention weights.  A sequence of
+        which the cache held rows is reported (``status``) and adds no weights."""
         o, *call = self._prepare(q, k, v, cu, None, o)
         self.append(k, v, cu)
         S.prompt_attention(*call)
@@ -71,7 +72,8 @@ class KV4State:
     def resume(self, q, k, v, cu, cu_kv, rows, o=None):
         """Packed prompts that go on over the cached rows.  cu_kv [B + 1] are the offsets of each
         sequence's cached and new rows together, ``rows`` their number in all.  Every row, the new ones
-        too, takes part as the value its codes stand for."""
+        too, takes part as the value its codes stand for.  A sequence whose rows are not as many as
+        cu_kv says is reported (``status``) and adds no weights."""
         if cu_kv is None:
             raise ValueError("cu_kv has the offsets of each sequence's cached and new rows together")
         kk, vv = (torch.zeros((rows, self.H_kv, self.d_h), dtype=q.dtype, device=q.device) for _ in range(2))
@@ -85,7 +87,8 @@ class KV4State:
         """A prompt's outputs, arguments and workspace.  What the call would refuse is refused here, before its
         rows are appended."""
         o = torch.empty_like(q) if o is None else o
-        a = S.make_prompt_args(q, k, v, o, cu, cu_kv, weight=self.weight, dev_status=self.status)
+        a = S.make_prompt_args(q, k, v, o, cu, cu_kv, weight=self.weight, dev_status=self.status,
+                               weight_len=self.len)
         # made without its workspace, which one with weights needs and which is looked at last, it launches nothing
         status = S.lib.spatten_prompt_attention(C.byref(a), None, 0, None)
         if status != S.E_WORKSPACE:

@@ -70,7 +70,7 @@ class prompt_args(C.Structure):
                 ("cu_q", vp), ("cu_kv", vp), ("dtype", i32), ("q", vp), ("q_ld_tok", i64),
                 ("k", vp), ("v", vp), ("kv_ld_tok", i64), ("o", vp), ("o_ld_tok", i64), ("sm_scale", f32),
                 ("weight", vp), ("weight_ld_seq", i64), ("weight_ld_head", i64), ("weight_cap", i32),
-                ("dev_status", vp), ("kernel", i32)]
+                ("dev_status", vp), ("kernel", i32), ("weight_len", vp)]
 
 
 class kv4_cache(C.Structure):
@@ -339,10 +339,10 @@ def _run(fn, name, device, stream, *args):
 
 
 def make_prompt_args(q, k, v, o, cu_q, cu_kv=None, weight=None, sm_scale=0.0, dev_status=None,
-                     kernel=ATTN_AUTO) -> prompt_args:
+                     kernel=ATTN_AUTO, weight_len=None) -> prompt_args:
     """Arguments of ``prompt_attention`` from torch tensors: q, o [rows, H, d_h] and k, v [rows, H_kv, d_h]
     (the heads of a row contiguous, the rows at any stride), cu_q, cu_kv int32 [B + 1], weight
-    float32 [B, H_kv, n].  The tensors are kept alive by the result."""
+    float32 [B, H_kv, n], weight_len int32 [B].  The tensors are kept alive by the result."""
     for t in (q, k, v, o):
         if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
             raise ValueError("q, k, v and o are [rows, heads, d_h] with the heads of a row contiguous")
@@ -351,18 +351,21 @@ def make_prompt_args(q, k, v, o, cu_q, cu_kv=None, weight=None, sm_scale=0.0, de
     if not (q.dtype == k.dtype == v.dtype == o.dtype):
         raise TypeError("q, k, v and o have one dtype")
     a = prompt_args()
-    a._device = _one_device(q, k, v, o, cu_q, cu_kv, weight, dev_status)
+    a._device = _one_device(q, k, v, o, cu_q, cu_kv, weight, dev_status, weight_len)
     a.B, a.H, a.H_kv, a.d_h = _i32_vector(cu_q, "cu_q") - 1, q.shape[1], k.shape[1], q.shape[2]
     if cu_kv is not None and _i32_vector(cu_kv, "cu_kv") != a.B + 1:
         raise ValueError("cu_kv and cu_q have the same length")
+    if weight_len is not None and _i32_vector(weight_len, "weight_len") != a.B:
+        raise ValueError("weight_len has one entry per sequence")
     a.total_q, a.total_kv, a.cu_q, a.cu_kv, a.dtype = q.shape[0], k.shape[0], ptr(cu_q), ptr(cu_kv), dtype_code(q)
     a.q, a.q_ld_tok, a.k, a.v, a.kv_ld_tok = ptr(q), _row_stride(q), ptr(k), ptr(v), _row_stride(k)
     a.o, a.o_ld_tok, a.sm_scale, a.dev_status, a.kernel = ptr(o), _row_stride(o), sm_scale, ptr(dev_status), kernel
+    a.weight_len = ptr(weight_len)
     if weight is not None:
         _dense_f32(weight, (a.B, a.H_kv), "weight")
         a.weight, a.weight_ld_seq, a.weight_ld_head, a.weight_cap = (
             ptr(weight), weight.stride(0), weight.stride(1), weight.shape[2])
-    a._keep = (q, k, v, o, cu_q, cu_kv, weight, dev_status)
+    a._keep = (q, k, v, o, cu_q, cu_kv, weight, dev_status, weight_len)
     return a
 
 

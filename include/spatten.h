@@ -375,6 +375,9 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  *    a sequence a non-finite row of K or V makes every output of its sequence and head unreliable; a NaN in a
  *    query row makes its output, and the weights of the keys that it sees, NaN.
  *  - weight rows j >= weight_cap are not written and reported (SPATTEN_E_INDEX).
+ *  - weight_len, where it is given, is what the caller's cache holds of each sequence, the rows of this call
+ *    among them.  A sequence with query rows whose n_kv is another (n_kv past weight_cap counts as weight_cap) is
+ *    reported (SPATTEN_E_INDEX) and adds no weight: its keys are not the cache's rows.
  *  - o overlaps none of the inputs.
  *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
  *  strides; workspace of spatten_prompt_workspace_size() bytes (it may be 0), which holds only this call's
@@ -404,6 +407,7 @@ typedef struct spatten_prompt_args {
   int32_t weight_cap;         /* rows j < weight_cap exist                                     */
   int32_t* dev_status;        /* device int32 or NULL                                          */
   int32_t kernel;             /* spatten_attn_kernel: AUTO, CUDA_CORE or TENSOR_CORE (bfloat16)  */
+  const int32_t* weight_len;  /* device [B] or NULL: rows of each sequence that weight counts   */
 } spatten_prompt_args;
 
 size_t spatten_prompt_workspace_size(const spatten_prompt_args* a);

@@ -106,3 +106,59 @@ def test_attention_float32_sums_do_not_drift(cuda, d, B):
     assert int(status.item()) == 0
     assert abs(rel.mean()) <= 2.0 ** -21 and np.abs(rel).max() <= 2.0 ** -19
     assert abs(host(w).sum() / p.sum() - 1) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
+def test_prompt_over_rows_and_resume_of_other_counts_are_reported(cuda, dtype, H, Hk):
+    """A prompt's weights belong to an empty sequence's first rows, a resumed one's to as many rows as the cache
+    holds: elsewhere they would go to other tokens' rows.  Such sequences are reported and add none; those next
+    to them, one without new rows among them, are served."""
+    from cascade_token_head_b200.kv4 import KV4State
+    S, d, B = lib(), 64, 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda r, h: torch.randn((r, h, d), generator=g, device="cuda").to(dtype)
+    st = KV4State(B, H, Hk, d, 64)
+    st.prompt(rnd(30, H), rnd(30, Hk), rnd(30, Hk), i32([0, 20, 30, 30]))
+    assert int(st.status.item()) == 0 and st.len.tolist() == [20, 10, 0]
+    w = st.weight.clone()
+    q, k, v = rnd(12, H), rnd(12, Hk), rnd(12, Hk)
+    st.prompt(q, k, v, i32([0, 0, 5, 12]))                    # sequence 1 held rows, 2 held none
+    assert int(st.status.item()) == S.E_INDEX and st.len.tolist() == [20, 15, 7]
+    assert torch.equal(st.weight[:2], w[:2])
+    _, add = R.prompt_attention(host(q)[5:], host(k)[5:], host(v)[5:], [0, 7], [0, 7], 64)
+    check_weight(host(st.weight)[2], 0.0, add[0], score_step(host(q), host(k), 7))
+    st.status.zero_()
+    w = st.weight.clone()
+    st.resume(rnd(3, H), rnd(3, Hk), rnd(3, Hk), i32([0, 1, 2, 3]), i32([0, 21, 37, 44]), 44)   # sequence 2: 7 for 8
+    assert int(st.status.item()) == S.E_INDEX and st.len.tolist() == [21, 16, 8]
+    assert torch.equal(st.weight[2], w[2]) and (st.weight[:2] != w[:2]).any(2).all()
+    st.status.zero_()
+    st.resume(rnd(3, H), rnd(3, Hk), rnd(3, Hk), i32([0, 1, 2, 3]), i32([0, 22, 39, 48]), 48)
+    assert int(st.status.item()) == 0
+    st = KV4State(B, H, Hk, d, 16)                            # rows that do not fit are dropped, the others' weights are kept
+    q, k, v = rnd(25, H), rnd(25, Hk), rnd(25, Hk)
+    st.prompt(q, k, v, i32([0, 20, 25, 25]))
+    assert int(st.status.item()) == S.E_INDEX and st.len.tolist() == [16, 5, 0]
+    _, add = R.prompt_attention(host(q), host(k), host(v), [0, 20, 25], [0, 20, 25], 16)
+    check_weight(host(st.weight)[:2], 0.0, add, score_step(host(q), host(k), 20))
+
+
+@pytest.mark.parametrize("dtype,kernel", [(BF, 0), (BF, 1), (F32, 0), (F32, 1)])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (6, 2)])
+def test_prompt_weights_of_counted_rows(cuda, dtype, kernel, H, Hk):
+    S = lib()
+    lens, kv = [5, 0, 140, 3], [40, 9, 140, 3000]
+    p = Prompt(S, dtype, 64, H, Hk, lens, kv, seed=3, kernel=kernel)
+    held = i32([40, 1, 139, 3000])
+    p.args = S.make_prompt_args(p.q, p.k, p.v, p.o, i32(p.cu_q), i32(p.cu_kv), weight=p.w, dev_status=p.status, kernel=kernel, weight_len=held)
+    p.run()
+    assert int(p.status.item()) == S.E_INDEX and torch.equal(p.w[2], p.w0[2])
+    q, k, v = host(p.q), host(p.k), host(p.v)
+    _, w = R.prompt_attention(q, k, v, p.cu_q, p.cu_kv, p.n_w)
+    w[2] = 0
+    check_weight(host(p.w), host(p.w0), w, score_step(q, k, 3000))
+    held.copy_(i32([40, 1, 140, 3000]))
+    p.w.copy_(p.w0)
+    p.status.zero_()
+    p.run().check(UBF if dtype == BF and kernel == 0 else 0.0)
