@@ -40,10 +40,12 @@ class KV4State:
 
     def _workspace(self, key, nbytes):
         """A workspace of the state's own for one kind of call: calls of one state run in order.  One that
-        becomes too small stays alive, since a captured graph may hold its address."""
+        becomes too small stays alive, since a captured graph may hold its address (or another stream still use
+        it); the next one is at least twice as large, so that all of them stay below four times the largest need."""
         held = self._ws.setdefault(key, [])
         if not held or held[-1].numel() < nbytes:
-            held.append(torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.k_codes.device))
+            size = max(nbytes, 256, 2 * held[-1].numel() if held else 0)
+            held.append(torch.empty(size, dtype=torch.uint8, device=self.k_codes.device))
         return held[-1]
 
     def append(self, k, v, cu=None):

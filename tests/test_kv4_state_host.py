@@ -62,3 +62,20 @@ def test_a_state_that_no_attention_takes_is_refused(made, h, hk, d):
     kv4, _ = made
     with pytest.raises(ValueError):
         kv4.KV4State(B, h, hk, d, CAP, device="cpu")
+
+
+def test_workspaces_of_a_growing_history_stay_bounded(made):
+    """Turn after turn of resume() needs a little more workspace: all that is held stays below four times the
+    largest need, and what an earlier call was given stays where it is."""
+    kv4, _ = made
+    st = kv4.KV4State(1, H, HK, D, 4096, device="cpu")
+    given = []
+    ask = st._workspace
+    st._workspace = lambda key, nb: (given.append((ask(key, nb), nb)), given[-1][0])[1]
+    for n in range(20, 4000, 20):
+        st.resume(rows(20, H), rows(20, HK), rows(20, HK), i32(0, 20), i32(0, n), n)
+    need = max(nb for _, nb in given)
+    assert all(ws.numel() >= nb for ws, nb in given) and len({nb for _, nb in given}) > 100
+    held = [w for ws in st._ws.values() for w in ws]
+    assert sum(w.numel() for w in held) <= 4 * need
+    assert {w.data_ptr() for w, _ in given} == {w.data_ptr() for w in held}
