@@ -378,6 +378,8 @@ int32_t spatten_cascade_forward(const spatten_cascade_cfg* cfg, const spatten_la
  *  - weight_len, where it is given, is what the caller's cache holds of each sequence, the rows of this call
  *    among them.  A sequence with query rows whose n_kv is another (n_kv past weight_cap counts as weight_cap) is
  *    reported (SPATTEN_E_INDEX) and adds no weight: its keys are not the cache's rows.
+ *  - Sums are of probabilities not yet normalised, which may be 2^8 large: they are finite while |v| is below
+ *    2^120 / n_kv.
  *  - o overlaps none of the inputs.
  *  Requirements: d_h 64 or 128, H a multiple of H_kv, B <= 65535, 16-byte aligned pointers and row
  *  strides; workspace of spatten_prompt_workspace_size() bytes (it may be 0), which holds only this call's
@@ -474,6 +476,8 @@ int32_t spatten_kv4_read(const spatten_kv4_cache* c, const int32_t* cu, const in
  * j < len[b], with grouped heads as above:
  *   O = softmax(sm_scale * q . k_j) . v_j;  with update_weight != 0, weight[b][h_kv][j] += the sum of
  *   the group's probabilities of row j.
+ * Finite while the rows' values are below 2^120 / len[b] in magnitude (the sums are of probabilities not yet
+ * normalised, which may be 2^8 large).
  * O = 0 for an empty sequence.  n_max bounds the lengths of this call (n_max <= cap; a longer
  * sequence is cut there and reported).  Sums are made in a fixed order (reruns are bit-identical).
  * Workspace: spatten_kv4_attention_workspace_size() bytes, intermediates of this call only.

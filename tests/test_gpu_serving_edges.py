@@ -162,3 +162,95 @@ def test_prompt_weights_of_counted_rows(cuda, dtype, kernel, H, Hk):
     p.w.copy_(p.w0)
     p.status.zero_()
     p.run().check(UBF if dtype == BF and kernel == 0 else 0.0)
+
+
+def norm_error(got, ref):
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+# A float32 call with scores below about 4 errs by independent roundings: of a score (2**-24 of it from each of the
+# query's terms, the product and its scaling, 2**-22 in all), its exponential (2**-22), sums of partial sums that
+# are much smaller than 2**-24 times their number, the quotient.  Their root mean square over all outputs is below
+# 2**-21; 2**-20 is left.  An operand term that gets lost costs 2**-16 or more (the bfloat16 terms: 2**-8, 2**-16
+# of a value; the query's fp16 terms: 2**-11).  The CUDA-core prompt kernel adds a row's n products one by one: sums
+# of terms of both signs grow like the root of their number, so step k rounds by at most 2**-24 sqrt(k / n) of the
+# result, and the root of the sum of their squares is 2**-24 sqrt(n / 2) at most.
+FLOAT32_RMS = 2.0 ** -20
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("lens,kv", [([1500, 700], [1500, 700]), ([40], [6000]), ([300], [2300])])
+def test_prompt_float32_is_float32(cuda, d, kernel, lens, kv):
+    p = Prompt(lib(), F32, d, 4, 2, lens, kv, seed=d, kernel=kernel)
+    p.qb *= 0.15
+    p.run()
+    ref, w = R.prompt_attention(host(p.q), host(p.k), host(p.v), p.cu_q, p.cu_kv, p.n_w)
+    assert norm_error(host(p.o), ref) <= FLOAT32_RMS + (U32 * (max(kv) / 2) ** 0.5 if kernel else 0.0)
+    assert norm_error(host(p.w), host(p.w0) + w) <= FLOAT32_RMS
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,n", [(1, 2, 20000), (3, 32, 5000), (1, 4, 300)])
+def test_attention_float32_is_float32(cuda, d, B, H, n):
+    S, Hk = lib(), 2
+    r = np.random.default_rng(n)
+    code = lambda: r.integers(-7, 8, (Hk, n, d))
+    scale = lambda: R.to_bf16(np.exp(r.normal(0, 0.3, (Hk, n, d // 32))))
+    kc, vc, ks, vs = code(), code(), scale(), scale()
+    dev = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda().expand(B, *a.shape).contiguous()
+    w = torch.zeros((B, Hk, n), device="cuda")
+    c = S.make_kv4_cache(dev(R.pack4(kc, 8), torch.uint8), dev(ks, BF), dev(R.pack4(vc, 4), torch.uint8), dev(vs, BF), w)
+    k, v = (a * np.repeat(s.astype(np.float64), 32, -1) for a, s in ((kc, ks), (vc, vs)))
+    q = torch.randn((B, H, d), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda") * 0.15
+    o = torch.empty_like(q)
+    a = S.make_kv4_attn_args(c, q, o, i32([n] * B), n)
+    nb = S.kv4_attention_workspace_size(a)
+    S.kv4_attention(a, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    refs = [R.kv4_attention(host(q)[b], k, v, n) for b in range(B)]
+    assert norm_error(host(o), np.stack([x for x, _ in refs])) <= FLOAT32_RMS
+    assert norm_error(host(w), np.stack([x for _, x in refs])) <= FLOAT32_RMS
+
+
+# Values at the end of the range that the sums take (|v| < 2**120 / n): the first keys score 0 and all behind
+# score just under 2**8 times as much in probability, which the running maximum of the first keys lets pass.
+LAG = 7.9 * np.log(2)
+
+
+@pytest.mark.parametrize("dtype,kernel", [(BF, 0), (BF, 1), (F32, 0), (F32, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q,n", [(2, 2000), (600, 600)])
+def test_prompt_largest_values(cuda, dtype, kernel, d, n_q, n):
+    p = Prompt(lib(), dtype, d, 2, 2, [n_q], [n], seed=1, kernel=kernel)
+    p.qb.zero_()
+    p.kb.zero_()
+    p.q[:, :, 0], p.k[128:, :, 0] = 1.0, LAG * d ** 0.5
+    p.vb.copy_(0.98 * 2.0 ** 120 / n * (1 - 0.02 * torch.rand(p.vb.shape, device="cuda")))
+    p.run().check(UBF if dtype == BF and kernel == 0 else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,n", [(1, 2000), (160, 3000)])
+def test_attention_largest_values(cuda, dtype, d, B, n):
+    S, Hk = lib(), 2
+    k, v = np.zeros((n, d), np.int64), np.full((n, d), 7)
+    k[:, 0] = 7
+    ks, vs = np.ones((n, d // 32)), np.full((n, d // 32), R.to_bf16(0.98 * 2.0 ** 120 / n / 7))
+    ks[:300] = 2.0 ** -20
+    ks[300:] = R.to_bf16(LAG * d ** 0.5 / 7)
+    dev = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda().expand(B, Hk, *a.shape).contiguous()
+    c = S.make_kv4_cache(dev(R.pack4(k, 8), torch.uint8), dev(ks, BF), dev(R.pack4(v, 4), torch.uint8), dev(vs, BF),
+                         torch.zeros((B, Hk, n), device="cuda"))
+    q = torch.zeros((B, 4, d), device="cuda", dtype=dtype)
+    q[:, :, 0] = 1
+    o = torch.empty_like(q)
+    a = S.make_kv4_attn_args(c, q, o, i32([n] * B), n)
+    nb = S.kv4_attention_workspace_size(a)
+    S.kv4_attention(a, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    kv = [np.broadcast_to(x * np.repeat(s, 32, -1), (Hk, n, d)) for x, s in ((k, ks), (v, vs))]
+    ref, w = R.kv4_attention(host(q)[0], *kv, n)
+    e = score_step(host(q)[0], kv[0], n)
+    for b in (0, B - 1):
+        check_out(host(o)[b], ref, np.abs(ref), e, dtype, UBF if dtype == BF else 2 * U32)
+        check_weight(host(c._keep[4])[b], 0.0, w, e)
