@@ -963,12 +963,17 @@ int32_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   const int64_t rows = a.in_place ? a.m : a.keep, pairs = static_cast<int64_t>(a.s.B) * a.s.H_kv;
   const size_t shared = evict_shared(a.n_max, a.keep, a.m);
   if (shared <= kEvictShared) {
-    // more CTAs while SMs are free and each has rows enough to move; large ones where one has an SM to itself, small
-    // ones, of which an SM holds four, where two an SM do not hold them all (512 heads, 1000 rows of 64 to 500: 33.9
-    // against 39.5 us with the middle size; 64 rows to 32: 13.5 against 19.7; but 224 heads, 2585 rows: 33.0 against 28.4)
+    // More CTAs while SMs are free and each has rows enough to move (half of 600 rows of 64, 64 heads: 8.2 us, with two
+    // CTAs a head 9.8; half of 2500 of 128, 8 heads: 16.3, with eight 10.6).  Clusters of eight wait for SMs of one
+    // part of the GPU and are taken up to 64 CTAs (16 heads, half of 10,000 rows of 128: 35.6, in fours 21.9; 8 heads
+    // 18.6, in fours 21.7).  Large CTAs where one has an SM to itself and the rows or the CTAs are many (32 heads, half
+    // of 10,000 rows: 22.3 against 32.6 with the middle size; 128 heads, half of 1200: 12.3 against 14.7; but 8 heads,
+    // half of 600: 9.5 against 7.7); small ones, of which an SM holds four, where two an SM do not hold them all (512
+    // heads, 1000 rows of 64 to 500: 33.9 against 39.5 with the middle size; 64 rows to 32: 13.5 against 19.7; but 224
+    // heads, 2585 rows: 33.0 against 28.4).
     int C = 1;
-    while (C < 8 && pairs * C * 2 <= sm_count() && rows >= 256 * C) C *= 2;
-    if (pairs * C <= sm_count() && a.n_max > 2048) return evict_one_launch<DH, 1024>(a, C, shared, st);
+    while (C < 8 && pairs * C * 2 <= (C < 4 ? sm_count() : 64) && rows >= 256 * C) C *= 2;
+    if (pairs * C <= sm_count() && (a.n_max > 2048 || pairs * C > 64)) return evict_one_launch<DH, 1024>(a, C, shared, st);
     return pairs * C <= 2 * sm_count() ? evict_one_launch<DH, 512>(a, C, shared, st) : evict_one_launch<DH, 256>(a, C, shared, st);
   }
   SPT_TRY(launch_chained(kv4_select_kernel, dim3(a.s.H_kv, a.s.B), dim3(kSelThreads), 0, st, 1, a));

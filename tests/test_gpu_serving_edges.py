@@ -7,7 +7,7 @@ import torch
 
 import serving_helpers as R
 from gpu_helpers import BF, lib
-from test_gpu_serving import F32, U32, UBF, Prompt, check_out, check_weight, host, i32, score_step
+from test_gpu_serving import Cache, F32, U32, UBF, Prompt, check_out, check_weight, host, i32, score_step
 
 pytestmark = pytest.mark.gpu
 
@@ -254,3 +254,27 @@ def test_attention_largest_values(cuda, dtype, d, B, n):
     for b in (0, B - 1):
         check_out(host(o)[b], ref, np.abs(ref), e, dtype, UBF if dtype == BF else 2 * U32)
         check_weight(host(c._keep[4])[b], 0.0, w, e)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,H,n,keep", [(1, 2, 5000, 2500), (2, 8, 3001, 1600), (4, 8, 1201, 600), (8, 8, 600, 299), (16, 8, 150, 75),
+                                        (12, 12, 1300, 1290)])
+def test_evict_every_cluster_size(cuda, in_place, B, H, n, keep):
+    """Few heads of many rows to many heads of few: one to eight CTAs a head, of each size."""
+    S, d, recent = lib(), 64, keep // 9
+    c = Cache(S, B, H, d, n, seed=B)
+    c.t["weight"].copy_(torch.round(c.t["weight"] * 16) / 16)      # ties
+    before = c.host()
+    dst = c if in_place else Cache(S, B, H, d, keep, seed=1)
+    ln = [n - 7 * b for b in range(B)]
+    held, status = i32(ln), i32([0])
+    out = held if in_place else torch.zeros_like(held)
+    nb = S.kv4_evict_workspace_size(c.c, n, keep)
+    S.kv4_evict(c.c, dst.c, held, out, i32(ln), n, keep, recent, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb, dev_status=status)
+    got = dst.host()
+    for b in range(B):
+        for h in range(0, H, 3):
+            src = R.evict_sources(before["weight"][b, h], before["pos"][b, h], ln[b], ln[b], keep, recent)
+            for key in got:
+                np.testing.assert_array_equal(got[key][b, h, :len(src)], before[key][b, h, src], err_msg=f"{key} {b} {h}")
+    assert out.tolist() == [min(x, keep) for x in ln] and int(status.item()) == 0
