@@ -190,9 +190,10 @@ __device__ __forceinline__ int v_word_at(int oct) {
 }
 
 // Packed rows: a warp takes runs of kSteps * 256 / DH rows of one head, eight channels a lane and step, all
-// loads before the first use: rows of a head are whole lines on both sides.  Bound by the quantization's
-// instructions (about half of the issue slots) and, next to them, by memory: 16,384 rows of 16 heads of 64 from
-// bfloat16 (86 MB) take 23 us, 3.7 TB/s.  Loading V's values before K's are codes spilled and gave nothing.
+// loads before the first use: rows of a head are whole lines on both sides.  A warp waits for memory, then quantizes,
+// and the warps that an SM holds hide half of that: 16,384 rows of 16 heads of 64 from bfloat16 (86 MB) take 24 us
+// by themselves, 3.6 TB/s (issue slots 56 %), from float32 (153 MB) 33 us, 4.6 TB/s.  Loading V's values before K's
+// are codes spilled and gave nothing.
 template <int DH> constexpr int kRowLanes = DH / 8;
 constexpr int kSteps = 4;
 constexpr int kChunks = 2, kReadChunks = 1;   // runs a warp: blocks that look their rows up, against blocks to even out
@@ -423,8 +424,9 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint3
                                             __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
-// A warp takes the rows of one head as the append kernel does, all loads before the first use.  Bound by
-// memory: 16,384 rows of 16 heads of 64 to bfloat16 (86 MB) take 17 us, 5.0 TB/s.
+// A warp takes the rows of one head as the append kernel does, all loads before the first use.  Three
+// quarters of what memory copies: 16,384 rows of 16 heads of 64 to bfloat16 (86 MB) take 17 us, 5.0 TB/s, to float32
+// (153 MB) 29 us, 5.2 TB/s; one run a warp, whose start and end nothing hides.
 template <int DH, typename T>
 __global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(ReadArgs a) {
   grid_dep_trigger();

@@ -16,7 +16,8 @@
 //            the code are larger and cost two bits.
 //   output   O^T[16 channels][8 heads] += codes . P', P' = exp(S - m) times the key's scale of the
 //            group, rounded to bfloat16 (its range is that of the scales) for bfloat16 queries and
-//            held as the sum of three bfloat16 (24 bits) for float32 ones; movmatrix turns P' from the
+//            held as the sum of three bfloat16 (24 bits) for float32 ones, whose products leave the tensor cores
+//            every 16 keys; movmatrix turns P' from the
 //            score layout into the operand's.  Codes become bfloat16 as 128 + u - 136, exact.
 // The tensor path is the register one since its operands are made in registers: a tcgen05 operand would
 // have to go through shared memory first, and the kernel is bound by memory and by the unpacking, not
@@ -24,9 +25,14 @@
 // In the cluster form scores stay in shared memory (in the workspace when they do not fit), so that the
 // weights need only one more exponential per score once the cluster has exchanged its maxima and sums.  Sums
 // are float32 in a fixed order.
-// What bounds them: 16 x 1152 rows of 16 heads of 64, 11.3 us a call, the chain of one CTA (query, tiles, joining,
-// weights: 13,500 cycles); 32 x 16,384 rows of 8 heads of 128 with 4 queries each (478 MB), 140 us, unpacking codes
-// (the split kernel, 122 us: ALU pipe 58 %, 4.1 TB/s) and reading the scores back for the weights (22 us).
+// Groups of nine to sixteen heads take two columns in one pass, larger ones several passes: 4 x 8192 rows of 4 heads
+// of 128 with 16 queries each 42 us (float32 45).  In bfloat16 at 128 channels two columns need more registers than
+// two CTAs an SM have (588 bytes spill); one CTA an SM took 31 us there, but 29 for 16 x 1152 rows against 22, and
+// passes of eight heads 34 and 20.
+// What bounds them: 16 x 1152 rows of 16 heads of 64, 11.6 us a call, the chain of one CTA (query, tiles, joining,
+// weights: 13,500 cycles); 32 x 16,384 rows of 8 heads of 128 with 4 queries each (478 MB), 142 us, of which the
+// split kernel takes 119 (no unit is full: 2.6 of 4 instructions a clock, ALU pipe 58 %, DRAM 51 %; a warp's chain
+// scores, vote, exponentials, product is what is left of the latency) and reading the scores back for the weights 22.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 

@@ -33,7 +33,7 @@ int32_t validate(const spatten_prompt_args& a) {
   return SPATTEN_OK;
 }
 
-// Tensor cores wherever they can run, down to single rows (float32: 16 prompts of 512, 16 heads of 64, 168 against
+// Tensor cores wherever they can run, down to single rows (float32: 16 prompts of 512, 16 heads of 64, 163 against
 // 570 us; 77 to 512 rows of 128 behind 1000 others, 145 against 603).
 bool use_tc(const spatten_prompt_args& a) { return a.kernel != SPATTEN_ATTN_CUDA_CORE && prompt_tc_supported(a); }
 

@@ -1,6 +1,6 @@
 // Prompt attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), bfloat16; float32 operands as
 // sums of three bfloat16 planes, which a first kernel splits them into, and six products of planes (24 bits;
-// 16 prompts of 512, 16 heads of 64: 168 us, and 570 with multiply-adds on CUDA cores).
+// 16 prompts of 512, 16 heads of 64: 163 us, and 570 with multiply-adds on CUDA cores).
 //
 // Two kernels, and a small third one when several query heads share a key/value head:
 //  OUTPUT  one pass over the visible keys in tiles of KT with the running maximum and sum of the
@@ -21,8 +21,10 @@
 // pipe, exp2_poly.cuh) next to the tensor cores.  8192 tokens, 32 heads of 128 over 8 (550 GFLOP): output
 // 487 us in a row of calls, 1127 TFLOP/s, where the power limit holds the clock down (440 us by itself, tensor pipe
 // 59 %); weights 299 (268; 55 %).  Short prompts are bound by each CTA's start and end and by the diagonal
-// tiles: a batch of 16, 41 and 28 us, tensor pipe 20 %.  O's rescaling is skipped while no row's maximum has
-// grown by more than 2^8, which float32 sums and the bfloat16 P bear without loss (P is relative).
+// tiles: a batch of 16, 39 and 29 us, tensor pipe 20 %.  Float32, 16 prompts of 512: 38 us to split the operands
+// (DRAM 63 %), 90 and 46 for outputs and weights, tensor pipe 39 %, with the softmax of a tile between its products.
+// O's rescaling is skipped while no row's maximum has grown by more than 2^8, which float32 sums and the bfloat16 P
+// bear without loss (P is relative; the values' range: spatten.h).
 // Every mbarrier wait is bounded: on timeout the CTA reports SPATTEN_E_TIMEOUT, waits for its own
 // copies and MMAs, frees its TMEM and returns.
 #include <cuda.h>
@@ -63,7 +65,7 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
   if constexpr ((Q & 3) < POLY) return exp2_poly2(x);
   else return ex2_pair(x);
 }
-constexpr int kWeightPoly = 1;   // of the weights' exponentials (8192 tokens: 316 us; none 341, half 337)
+constexpr int kWeightPoly = 1;   // of the weights' exponentials (outputs and weights of 16 x 1024 rows of 16 heads of 64: 117 us; none 121, half 121)
 
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // whether p holds in any of the threads that share a named barrier
@@ -371,8 +373,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) prompt_out_kernel(Promp
         commit_one(&bars.kv_empty[0]);
       }
       // One tile's P V and next scores run while the other tile's softmax does.  Between two tiles' MMAs there
-      // is only the wait for P: the tensor cores idle meanwhile.  (An MMA warp per tile was slower, 675 us
-      // against 519: the tiles' MMAs then alternate in the pipe.)
+      // is only the wait for P: the tensor cores idle meanwhile.  (An MMA warp per tile took 675 us where this
+      // form then took 519: the tiles' MMAs alternate in the pipe.)
       int sv = 1, sk = 2 % NST, pv = 0, pk = (2 / NST) & 1;   // the ring's stages of V(t) and K(t + 1), and their phases
       for (int t = 0; t < Tmax && !aborted; ++t) {
         const bool more = t + 1 < Tmax;
@@ -1039,8 +1041,8 @@ int64_t out_blocks(const spatten_prompt_args& a) {
 }
 
 // Splits of the key tiles: as many as leave all CTAs resident at once and each kSplitTiles tiles of a sequence of
-// average length (16 rows of 16 heads of 64 behind 8000 others: 23 against 111 us; 500 of 8 heads behind 1500: 21
-// against 32; float32, 16 of 8 heads of 128 behind 1000: 25, with four tiles at least 34, unsplit 63).
+// average length (outputs of 16 rows of 16 heads of 64 behind 8000 others: 21 against 111 us unsplit; 500 of 8 heads
+// behind 1500: 20 against 32; float32, 16 of 8 heads of 128 behind 1000: 24, with four tiles at least 33, unsplit 63).
 template <class O>
 int out_splits(const spatten_prompt_args& a) {
   const int64_t most = std::min<int64_t>(O::kCtas * sm_count() / std::max<int64_t>(1, out_blocks<O>(a)), a.total_kv / std::max(1, a.B) / (kSplitTiles * O::KT));
