@@ -286,30 +286,34 @@ def _check_device(device, *tensors):
 
 
 def _rows_dtype(device, dtype, *tensors) -> int:
-    """The dtype code that a call's row blocks, all on `device`, have (addresses are not looked at)."""
+    """The dtype code of a call's row blocks, all on `device` (addresses are not looked at): the one they have, or
+    the one given, of whose size their elements are."""
+    code = dtype
     for t in tensors:
         if t is None or type(t) is int:
             continue
         if t.get_device() != device:
             raise ValueError("the tensors of a call are on one device")
-        code = dtype_code(t)
-        if dtype is None:
-            dtype = code
-        elif dtype != code:
+        if dtype is not None:
+            same = t.element_size() == (2 if dtype == BF16 else 4)
+        else:
+            same = code is None or code == dtype_code(t)
+            code = dtype_code(t)
+        if not same:
             raise TypeError("the rows of a call have one dtype")
-    return dtype
+    return code
 
 
 _int32 = None   # torch.int32, set with the first cache (a lookup in `torch` costs 0.1 us a call)
 
 
 def _vector(t, n, device):
-    """Address of a vector of n counts, positions or offsets on `device` (None and addresses pass through)."""
+    """Address of a vector of at least n counts, positions or offsets on `device` (None and addresses pass through)."""
     if t is None or type(t) is int:
         return t
     if t.dtype is not _int32 or not t.is_contiguous():
         raise TypeError("counts, positions, offsets and status words are contiguous int32 vectors")
-    if t.numel() != n:
+    if t.numel() < n:
         raise ValueError(f"a vector has {t.numel()} entries where the call reads {n}")
     if t.get_device() != device:
         raise ValueError("the tensors of a call are on one device")
